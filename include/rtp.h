@@ -69,7 +69,8 @@ typedef enum {
   RTP_ERR_WORKSPACE = 5      /* ws too small or misaligned */
 } rtp_status;
 
-typedef enum { RTP_BF16 = 0, RTP_F32 = 1 } rtp_dtype;
+/* RTP_F16 (IEEE binary16) is taken by the serving calls, rtp_attn_packed and below. */
+typedef enum { RTP_BF16 = 0, RTP_F32 = 1, RTP_F16 = 2 } rtp_dtype;
 
 /* Element strides of a [B, N, H, D] tensor (D contiguous). */
 typedef struct { int64_t b, n, h; } rtp_strides;
@@ -532,6 +533,171 @@ RTP_API rtp_status rtp_swa(const void* q, rtp_strides qs, const void* k, rtp_str
                    int B, int Nq, int Nk, int q_pos0, int Hq, int Hkv,
                    const int32_t* heads, int n_heads, int window, float scale,
                    void* ws, size_t ws_bytes, rtp_stream_t stream);
+
+/* ========================================================================
+ * Serving: prompts of different lengths in one call, a paged key-value
+ * cache, and its eviction by accumulated attention weight.
+ *
+ * The calls above serve one padded batch (N a multiple of 64) and one
+ * contiguous cache of equal lengths. These serve a batch as it arrives:
+ *   packed tensors  [T, H, D]: S sequences one behind the other. cu_seqlens
+ *            (device int32 [S + 1], non-decreasing, within [0, T]) holds their
+ *            bounds: sequence i is rows cu_seqlens[i] .. cu_seqlens[i+1] - 1;
+ *            empty sequences are allowed, rows in no sequence are neither read
+ *            as keys nor written. Strides are rtp_strides {b (not read), n, h};
+ *            no row may overlap another (no stride of 0 over more than one).
+ *   paged cache  pages of page_size tokens (a power of two up to 65536) of
+ *            every KV head; slot s of sequence b is row s % page_size of page
+ *            table[b][s / page_size]. A slot whose page id lies outside
+ *            [0, num_pages) holds no token: readers skip it, writers leave it.
+ *            Its capacity, max_pages * page_size, is at most 2^30.
+ *   dtype    RTP_BF16 or RTP_F16, one for every 16-bit tensor of a call.
+ *            Scores, softmax statistics, sums and weights are fp32; the
+ *            softmax's numerators are rounded once to dtype for the product
+ *            with v, its denominator takes them unrounded.
+ * Lengths and offsets stay on the device, so a captured graph follows them.
+ * They are clamped to the limits passed from the host: bad contents give
+ * unspecified rows of the outputs, never an access outside the tensors.
+ * Keys that a row does not attend have no influence on it, whatever they
+ * hold (NaN and infinities included). Attended keys whose score is -inf weigh
+ * nothing; a row left with nothing is zero, its log-sum-exp -inf.
+ * Results do not depend on timing: no floating-point atomics.
+ */
+typedef struct {
+  void* k;                 /* device, 16-bit [num_pages, page_size, Hkv, D] with strides ks, D contiguous */
+  void* v;                 /* likewise with strides vs */
+  rtp_strides ks, vs;      /* element strides: b = page, n = row of a page, h = head; multiples of 8 */
+  float* weights;          /* device fp32 [num_pages, Hkv, page_size], contiguous, or NULL */
+  const int32_t* table;    /* device int32 [B, table_stride]: page ids, max_pages per sequence */
+  int64_t table_stride;
+  int32_t num_pages, page_size, max_pages, Hkv;
+} rtp_paged_cache;
+
+/*
+ * rtp_attn_packed - causal attention of packed prompts.
+ *   Row t of a sequence attends its rows u <= t with t - u < window:
+ *     o[t] = sum_u exp(scale q[t].k[u] - lse[t]) v[u],
+ *     lse[t] = ln sum_u exp(scale q[t].k[u]).
+ *   window as long as the longest sequence (or INT32_MAX) is the whole prefix:
+ *   retrieval heads without selection; a shorter one is the streaming heads'
+ *   sliding window, as rtp_swa.
+ *
+ *   q, o     dtype [T, Hq, D] device (strides qs, os); o is written only for
+ *            the listed heads and rows of sequences.
+ *   k, v     dtype [T, Hkv, D] device (strides ks, vs).
+ *   heads    host int32 [n_heads], distinct.
+ *   lse      fp32 [n_heads, T] device out, contiguous, or NULL; row j belongs
+ *            to heads[j], rows of sequences written.
+ *   T >= 0, S >= 1, Hq <= 256, window >= 1, scale > 0.
+ *   ws       rtp_workspace_size_attn_packed() bytes: the status word (see
+ *            rtp_get_device_status).
+ */
+RTP_API size_t rtp_workspace_size_attn_packed(void);
+RTP_API rtp_status rtp_attn_packed(const void* q, rtp_strides qs, const void* k, rtp_strides ks, const void* v,
+                                   rtp_strides vs, void* o, rtp_strides os, rtp_dtype dtype, int T, int Hq, int Hkv,
+                                   const int32_t* heads, int n_heads, const int32_t* cu_seqlens, int S, int window,
+                                   float scale, float* lse, void* ws, size_t ws_bytes, rtp_stream_t stream);
+
+/*
+ * rtp_attn_key_weights - the attention weight every key of packed prompts got.
+ *     weights[g, u] = sum over the listed heads h of KV head g and the last
+ *     n_obs rows t of u's sequence that attend u of
+ *     exp(scale q[t, h].k[u, g] - lse[h, t]).
+ *   n_obs at least the longest sequence sums whole columns of the attention
+ *   matrix; a small one observes what the prompts' last queries looked at.
+ *
+ *   q, k, dtype, heads, cu_seqlens, window, scale  as in rtp_attn_packed.
+ *   lse      fp32 [n_heads, T] device, as written by rtp_attn_packed; read
+ *            for the observed rows.
+ *   weights  fp32 [Hkv, T] device out, contiguous: rows of sequences, KV heads
+ *            with a listed head.
+ *   n_obs >= 1; limits as rtp_attn_packed.
+ *   ws       rtp_workspace_size_attn_key_weights() bytes: the status word.
+ */
+RTP_API size_t rtp_workspace_size_attn_key_weights(void);
+RTP_API rtp_status rtp_attn_key_weights(const void* q, rtp_strides qs, const void* k, rtp_strides ks,
+                                        rtp_dtype dtype, int T, int Hq, int Hkv, const int32_t* heads, int n_heads,
+                                        const int32_t* cu_seqlens, int S, const float* lse, int n_obs, int window,
+                                        float scale, float* weights, void* ws, size_t ws_bytes, rtp_stream_t stream);
+
+/*
+ * rtp_paged_append - puts the keys and values of new tokens into the cache:
+ * row t of sequence i goes to slot pos[i] + t - cu_seqlens[i] of table row i.
+ *   A prefill appends the whole packed K and V with pos = 0; a decode step
+ *   appends one row per sequence (cu_seqlens = 0, 1, .., B) at pos = length.
+ *
+ *   cache    host struct; k, v (and weights, if it has any) are written. The
+ *            slots written by one call must be distinct.
+ *   k, v     16-bit [T, Hkv, D] device (strides ks, vs), the cache's dtype.
+ *   weights  fp32 [Hkv, T] device, contiguous (rtp_attn_key_weights), or NULL:
+ *            the new tokens start at weight 0.
+ *   pos      device int32 [S]. Rows whose slot lies outside the capacity are
+ *            dropped.
+ *   T >= 0, S >= 1.
+ */
+RTP_API rtp_status rtp_paged_append(const rtp_paged_cache* cache, const void* k, rtp_strides ks, const void* v,
+                                    rtp_strides vs, const float* weights, int T, const int32_t* cu_seqlens, int S,
+                                    const int32_t* pos, rtp_stream_t stream);
+
+/*
+ * rtp_paged_attn_decode - one new token per sequence attends the paged cache.
+ *   Sequence b attends the slots {0 .. sink-1} U {len-window .. len-1}, each
+ *   once, len = lens[b] clamped to [0, max_len] (the new token's own key and
+ *   value are in the cache, see rtp_paged_append). window >= max_len attends
+ *   everything. A sequence of length 0 gets a zero row.
+ *
+ *   q, o     dtype [B, Hq, D] device (strides qs, os {b, n (not read), h});
+ *            o is written only for the listed heads.
+ *   lens     device int32 [B]; max_len (host) bounds them and the workspace,
+ *            1 <= max_len <= the cache's capacity.
+ *   heads    host int32 [n_heads], distinct.
+ *   lse      fp32 [B, n_heads] device out (natural log), or NULL.
+ *   weights_out  fp32 like cache->weights, or NULL: for every slot s < len and
+ *            every KV head with a listed head, weights_out = cache->weights +
+ *            the sum over the group's listed heads of the softmax weight of s
+ *            (0 where s is not attended). May be cache->weights itself. Pages
+ *            may then not be shared between the sequences of a call.
+ *   ws       rtp_workspace_size_paged_attn_decode(B, max_len, n_heads, window,
+ *            sink, weights_out != NULL) bytes; the status word always reads
+ *            RTP_OK (the kernels never wait on one another on the device).
+ *   Hq / Hkv <= 16, Hq <= 256, 1 <= B <= 65535, window >= 1, sink >= 0, scale > 0.
+ */
+RTP_API size_t rtp_workspace_size_paged_attn_decode(int B, int max_len, int n_heads, int window, int sink,
+                                                    int with_weights);
+RTP_API rtp_status rtp_paged_attn_decode(const void* q, rtp_strides qs, const rtp_paged_cache* cache,
+                                         const int32_t* lens, int max_len, void* o, rtp_strides os, rtp_dtype dtype,
+                                         int B, int Hq, const int32_t* heads, int n_heads, int window, int sink,
+                                         float scale, float* lse, float* weights_out, void* ws, size_t ws_bytes,
+                                         rtp_stream_t stream);
+
+/*
+ * rtp_cache_evict - shrinks a paged cache to `budget` tokens per sequence and
+ * KV head by accumulated attention weight.
+ *   A sequence of length len > budget keeps, per KV head, the slots
+ *   {0 .. sink-1}, {len-recent .. len-1} and, of the others, the
+ *   budget - sink - recent of largest weight (equal weights: the lower slot;
+ *   NaN ranks above every number). Kept slot number j (ascending) moves to
+ *   slot j: its K and V rows and its weight. Shorter sequences keep everything.
+ *   Heads keep different tokens, so afterwards a slot is no longer a position;
+ *   keys are expected with their positions already applied.
+ *
+ *   src, dst host structs, both with weights. dst == src, or an equal struct,
+ *            works in place (slots behind budget keep their old contents, and
+ *            sequences may not share pages); otherwise the pages that dst's
+ *            table names may not be among src's, and dst needs capacity for
+ *            min(budget, max_len) slots. The same table with only some of the
+ *            buffers shared is refused. dst may have another page size.
+ *   lens     device int32 [B], clamped to [0, max_len];
+ *            1 <= max_len <= src's capacity.
+ *   idx      int32 [B, Hkv, budget] device out: the kept slots, ascending, -1
+ *            padded.
+ *   new_lens int32 [B] device out: min(len, budget). Not `lens` itself, which
+ *            is read until the call's work is done (refused).
+ *   budget >= 1, sink, recent >= 0, sink + recent <= budget, B * Hkv <= 65535.
+ */
+RTP_API rtp_status rtp_cache_evict(const rtp_paged_cache* src, const rtp_paged_cache* dst, int B,
+                                   const int32_t* lens, int max_len, int budget, int sink, int recent, int32_t* idx,
+                                   int32_t* new_lens, rtp_stream_t stream);
 
 #ifdef __cplusplus
 }

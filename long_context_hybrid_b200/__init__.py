@@ -16,6 +16,10 @@ from typing import Optional, Sequence
 
 import torch
 
+from . import serving as _serving
+from .serving import (PagedCache, PagedLayer, Strides, attn_key_weights, attn_packed, cache_evict, paged_append,
+                      paged_attn_decode)
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "librtp.so")
 
@@ -25,10 +29,6 @@ D_HEAD, R_INDEX, BLOCK = 128, 16, 64
 
 class RtpError(RuntimeError):
     pass
-
-
-class Strides(ctypes.Structure):
-    _fields_ = [("b", ctypes.c_int64), ("n", ctypes.c_int64), ("h", ctypes.c_int64)]
 
 
 _lib = None
@@ -78,6 +78,7 @@ _SIGNATURES = {
     "rtp_workspace_size_swa": (_SZ, [_I, _I, _I, _I, _I]),
     "rtp_swa": (_I, [_P, Strides, _P, Strides, _P, Strides, _P, Strides, _I, _I, _I, _I, _I, _I,
                      _c_i32p, _I, _I, _F, _P, _SZ, _P]),
+    **_serving.SIGNATURES,
 }
 
 
@@ -608,4 +609,6 @@ __all__ = ["lib", "RtpError", "index_project", "index_append", "index_quantize",
            "sparse_attn_prefill", "triangle_prefill", "sparse_attn_decode", "swa", "decode_attn_hybrid",
            "decode_step", "decode_step_clustered",
            "PrefillLayer", "DecodeStep", "OrthrosStep",
+           "PagedCache", "PagedLayer", "attn_packed", "attn_key_weights", "paged_append", "paged_attn_decode",
+           "cache_evict",
            "kv_of", "LIB_PATH"]

@@ -5,6 +5,7 @@
 
 #include "../../include/rtp.h"
 #include "../../include/rtp_testing.h"
+#include "api_check.h"
 #include "attn_prefill_common.cuh"
 #include "rtp_common.cuh"
 #include "rtp_internal.h"
@@ -12,32 +13,6 @@
 using namespace rtp;
 
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
-bool stride_ok(rtp_strides s) { return s.b % 8 == 0 && s.n % 8 == 0 && s.h % 8 == 0 && s.b >= 0 && s.n >= 0 && s.h >= 0; }
-
-rtp_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RTP_OK : RTP_ERR_CUDA; }
-
-// The device must be a Blackwell datacenter part (compute capability 10.x).
-rtp_status check_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return RTP_ERR_CUDA;
-  int major = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return RTP_ERR_CUDA;
-  return major == 10 ? RTP_OK : RTP_ERR_UNSUPPORTED;
-}
-
-rtp_status check_heads(const int32_t* heads, int n, int H) {
-  if (!heads || n < 1 || n > kMaxHeads) return RTP_ERR_INVALID_ARG;
-  for (int i = 0; i < n; ++i)
-    if (heads[i] < 0 || heads[i] >= H) return RTP_ERR_INVALID_ARG;
-  for (int i = 0; i < n; ++i)
-    for (int k = i + 1; k < n; ++k)
-      if (heads[i] == heads[k]) return RTP_ERR_INVALID_ARG;
-  return RTP_OK;
-}
 
 // Tensor maps for q/k/v and the tcgen05 launch; the status word (first 4 bytes
 // of ws) is cleared on the stream first and set by a CTA whose wait ran out.

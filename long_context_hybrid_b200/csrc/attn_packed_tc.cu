@@ -1,0 +1,450 @@
+// Causal attention of packed prompts on the 5th-generation tensor cores
+// (tcgen05 + TMEM + TMA): sequences of any lengths one behind the other, each
+// head over its whole prefix or its last `window` keys.
+//
+//   o[t] = sum_u p_u v_u,  p_u = exp(scale q[t].k[u] - lse[t]),
+//   u in t's sequence, u <= t, t - u < window.
+//
+// A CTA computes 256 consecutive query rows of one sequence and head against
+// tiles of 128 keys aligned to the sequence's start. The lengths stay on the
+// device: the grid covers every tile number that any lengths could need, and
+// a CTA finds its sequence by a search of the offsets; numbers run downwards, so that
+// within a sequence the rows with most keys start first.
+//
+// Warp roles (384 threads):
+//   warp 0     TMA producer: two Q tiles, then K and V tiles (32 KB each,
+//              128-byte swizzle) through a ring of five: a stage holds either, so
+//              the ring is two and a half key tiles deep beside 64 KB of Q;
+//   warp 1     TMEM owner and MMA issuer: S_t = Q_t K^T (M128 N128 K128) and
+//              O_t += P_t V (P from TMEM, V MN-major), in the order
+//              PV0 QK0' PV1 QK1', so that one tile's products run under the
+//              other's softmax; a query tile takes only the key tiles that it attends;
+//   warps 2, 3 V guard: in key tiles that a mask cuts, rows behind the sequence's
+//              end and non-finite values are zeroed before the product (there
+//              P is 0, and 0 * NaN would reach rows that do not attend the
+//              key); the epilogue puts non-finite values back into the rows
+//              that do attend them;
+//   warps 4-11 softmax, one warpgroup per query tile, one row per thread:
+//              running maximum in the log2 domain with lazy rescaling of O (only
+//              when the maximum grows by more than 8, so P stays below 2^8, within the
+//              range of both 16-bit types), row sum in fp32 from the
+//              unrounded exponentials, P rounded to the input type over S in TMEM.
+// Every wait is bounded, as in the other tensor-core kernels.
+#include "attn_packed_common.cuh"
+#include "paged.cuh"
+#include "sm100.cuh"
+
+namespace rtp {
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTileRows = 256;                       // query rows of a CTA
+constexpr int kKeyTile = 128;
+constexpr int kRing = 5;
+constexpr uint32_t kStage = 32768;                   // one K or V tile: [D half][128 rows][128 B]
+constexpr uint32_t kRingOff = 2 * kStage;            // behind the two Q tiles
+constexpr uint32_t kTmemCols = 512;                  // tile t: S at 256 t, O at 256 t + 128
+constexpr int kStatusTimeout = 4;
+
+struct PackedParams {
+  void* o; int64_t o_sn, o_sh;
+  const void* v; int64_t v_sn, v_sh;                 // for the epilogue's non-finite values
+  const int32_t* cu;
+  float* lse;                                        // [n_heads, T] or NULL
+  int S, T, G, window, n_heads;
+  int64_t n_numbers;                                 // tile numbers: floor(T / 256) + S
+  float scale_log2;
+  uint8_t head[kMaxHeads];
+};
+
+struct Bars {
+  uint64_t q_full[2], full[kRing], empty[kRing], v_ok[kRing];
+  uint64_t s_full[2], p_full[2], fin;
+  uint32_t tmem_base;
+  int abort;
+  int poison;                                        // the guard met a non-finite value of the sequence
+};
+
+constexpr size_t kSmemBytes = 1024 + kRingOff + kRing * kStage + sizeof(Bars);
+
+// Halves of a pair whose exponent is all ones, as bits 15 and 31.
+template <bool F16>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
+  return F16 ? ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u : ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+}  // namespace
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant__ CUtensorMap tmQ,
+                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, int* status) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  Bars& bars = *reinterpret_cast<Bars*>(smem + kRingOff + kRing * kStage);
+  volatile int* abort_flag = &bars.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int jh = blockIdx.x % p.n_heads;
+  const int h = p.head[jh], g = h / p.G;
+  int c0, n, row0;                                   // the sequence's first row and length, the CTA's first row in it
+  if (!packed_tile(p.cu, p.S, p.T, kTileRows, p.n_numbers - 1 - blockIdx.x / p.n_heads, &c0, &n, &row0)) return;
+
+  // key tiles kt_lo .. kt_lo + n_tiles - 1 (of 128 keys); query tile t takes
+  // those of [first[t], last[t])
+  const int window = p.window;
+  int first[2], last[2];
+  const int kt_lo = max(0, row0 - window + 1) / kKeyTile;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int r = row0 + t * 128;
+    const bool any = r < n;
+    first[t] = any ? max(0, r - window + 1) / kKeyTile - kt_lo : 0;
+    last[t] = any ? min(n - 1, r + 127) / kKeyTile + 1 - kt_lo : 0;
+  }
+  const int n_tiles = max(last[0], last[1]);
+  const int row_last = min(n - 1, row0 + kTileRows - 1);
+  // a tile of which some row of the CTA does not attend some key
+  auto masked = [&](int j) {
+    const int k0 = (kt_lo + j) * kKeyTile;
+    return k0 + kKeyTile - 1 > row0 || k0 <= row_last - window;
+  };
+
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&bars.q_full[t]), 1);
+      mbar_init(smem_u32(&bars.s_full[t]), 1);
+      mbar_init(smem_u32(&bars.p_full[t]), 128);
+    }
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(smem_u32(&bars.full[s]), 1);
+      mbar_init(smem_u32(&bars.empty[s]), 1);
+      mbar_init(smem_u32(&bars.v_ok[s]), 2);
+    }
+    mbar_init(smem_u32(&bars.fin), 1);
+    bars.abort = 0;
+    bars.poison = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch(&tmQ);
+      tma_prefetch(&tmK);
+      tma_prefetch(&tmV);
+      auto load_q = [&](int t) {
+        const uint32_t bar = smem_u32(&bars.q_full[t]);
+        mbar_arrive_expect_tx(bar, kStage);
+        tma_load_4d(sb + t * kStage, &tmQ, bar, 0, h, c0 + row0 + t * 128, 0);
+        tma_load_4d(sb + t * kStage + 16384, &tmQ, bar, 64, h, c0 + row0 + t * 128, 0);
+      };
+      load_q(0);
+      int issued = 0;
+      for (int r = 0; r < 2 * n_tiles; ++r) {        // item 2j is K of tile j, 2j + 1 its V
+        const int s = r % kRing;
+        if (r >= kRing && !mbar_wait(smem_u32(&bars.empty[s]), (r / kRing - 1) & 1, abort_flag)) break;
+        const uint32_t dst = sb + kRingOff + s * kStage, bar = smem_u32(&bars.full[s]);
+        const CUtensorMap* map = (r & 1) ? &tmV : &tmK;
+        const int key = c0 + (kt_lo + (r >> 1)) * kKeyTile;
+        mbar_arrive_expect_tx(bar, kStage);
+        tma_load_4d(dst, map, bar, 0, g, key, 0);
+        tma_load_4d(dst + 16384, map, bar, 64, g, key, 0);
+        issued = r + 1;
+        if (r == 0 && last[1] > 0) load_q(1);
+      }
+      // The MMA side ends every path by committing `fin`; after an abort the
+      // copies that nobody consumed are waited for, with a short bound.
+      {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(smem_u32(&bars.fin), 0) && !*abort_flag && clock64() - t0 < kWaitLimitCycles) {
+        }
+      }
+      if (*abort_flag) {
+        wait_short(smem_u32(&bars.q_full[0]), 0);
+        if (last[1] > 0 && issued > 0) wait_short(smem_u32(&bars.q_full[1]), 0);
+        for (int r = max(0, issued - kRing); r < issued; ++r)
+          wait_short(smem_u32(&bars.full[r % kRing]), (r / kRing) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      bool ok = true;
+      auto full = [&](int r) { return mbar_wait(smem_u32(&bars.full[r % kRing]), (r / kRing) & 1, abort_flag); };
+      for (int j = -1; ok && j < n_tiles; ++j) {
+        const int kr = 2 * (j + 1), vr = 2 * j + 1;
+        const uint32_t k_s = sb + kRingOff + (uint32_t)(kr % kRing) * kStage;
+        const uint32_t v_s = sb + kRingOff + (uint32_t)((vr + kRing) % kRing) * kStage;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j >= first[t] && j < last[t]) {
+            // v_ok of every tile, so that the guard never falls a ring behind
+            ok = ok && mbar_wait(smem_u32(&bars.p_full[t]), (j - first[t]) & 1, abort_flag) && full(vr) &&
+                 mbar_wait(smem_u32(&bars.v_ok[vr % kRing]), (vr / (2 * kRing)) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv<F16>(tmem + t * 256u + 128u, tmem + t * 256u, v_s, j > first[t]);
+          }
+          if (t == 1 && j >= 0) mma_commit(smem_u32(&bars.empty[vr % kRing]));
+          if (j + 1 >= first[t] && j + 1 < last[t]) {
+            ok = ok && (j + 1 > first[t] || mbar_wait(smem_u32(&bars.q_full[t]), 0, abort_flag)) && full(kr);
+            if (!ok) break;
+            tc_fence_after();
+            issue_qk<F16>(tmem + t * 256u, sb + t * kStage, k_s);
+            mma_commit(smem_u32(&bars.s_full[t]));
+          }
+          if (t == 1 && j + 1 < n_tiles) mma_commit(smem_u32(&bars.empty[kr % kRing]));
+        }
+      }
+      mma_commit(smem_u32(&bars.fin));
+      wait_short(smem_u32(&bars.fin), 0);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ V guard
+    const int gt = tid - 64;
+    for (int j = 0; j < n_tiles; ++j) {
+      const int r = 2 * j + 1, s = r % kRing;
+      const bool w = mbar_wait(smem_u32(&bars.full[s]), (r / kRing) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, w)) break;
+      if (masked(j)) {
+        uint4* tile = reinterpret_cast<uint4*>(smem + kRingOff + s * kStage);
+        const int there = n - (kt_lo + j) * kKeyTile;     // rows of the tile that are keys of the sequence
+        bool met = false;
+#pragma unroll 8
+        for (int x = gt; x < (int)(kStage / 16); x += 64) {
+          uint4 d = tile[x];
+          const uint32_t a = nonfinite_bits<F16>(d.x), b = nonfinite_bits<F16>(d.y), c = nonfinite_bits<F16>(d.z),
+                         e = nonfinite_bits<F16>(d.w);
+          if (a | b | c | e) {
+            met = met || ((x >> 3) & 127) < there;
+            d.x &= ~((a >> 15) * 0xffffu); d.y &= ~((b >> 15) * 0xffffu);
+            d.z &= ~((c >> 15) * 0xffffu); d.w &= ~((e >> 15) * 0xffffu);
+            tile[x] = d;
+          }
+        }
+        if (met) bars.poison = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(smem_u32(&bars.v_ok[s]));
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;                  // query tile of this warpgroup
+    const int r = (warp & 3) * 32 + lane;           // row within the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int i = row0 + t * 128 + r;               // row within the sequence
+    const float sl2 = p.scale_log2;
+    const uint32_t s_addr = tmem + lane_off + t * 256u, o_addr = s_addr + 128u;
+    const int j0 = first[t], j1 = last[t];
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = j1 > j0;
+    for (int j = j0; j < j1; ++j) {
+      const bool w = mbar_wait(smem_u32(&bars.s_full[t]), (j - j0) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+      tc_fence_after();
+      // Each 64-key half: mask, a lazy update of the maximum, exponentials, and
+      // P written as 16-bit pairs over S columns [32 half, 32 half + 32). If the
+      // second half raises the maximum by more than 8, the first half's P is
+      // rescaled in TMEM.
+      float o_factor = 1.f;
+      bool o_scaled = false;
+      float sum_a = 0.f, sum_b = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int key0 = (kt_lo + j) * kKeyTile + half * 64;
+        const bool none = key0 > i || key0 + 63 <= i - window;
+        const bool all = key0 + 63 <= i && key0 > i - window;
+        uint32_t v[64];
+        tmem_ld32(s_addr + half * 64u, v);
+        tmem_ld32(s_addr + half * 64u + 32u, v + 32);
+        tc_wait_ld();
+        if (!none && !all) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (key0 + c > i || key0 + c <= i - window) v[c] = __float_as_uint(-INFINITY);
+        }
+        float mx = -INFINITY;
+        if (!none) {
+          float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            a0 = max3f(a0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+            a1 = max3f(a1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+          }
+          mx = fmaxf(a0, a1);
+        }
+        const float m_cand = mx * sl2;
+        const bool need = m_cand > m_run + 8.f;
+        if (half == 1 && __any_sync(0xffffffffu, need && m_run != -INFINITY)) {
+          const float f = (need && m_run != -INFINITY) ? ex2(m_run - m_cand) : 1.f;
+          uint32_t x[32];
+          tmem_ld32(s_addr, x);
+          tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = Elem16<F16>::pack(Elem16<F16>::lo(x[c]) * f, Elem16<F16>::hi(x[c]) * f);
+          tmem_st32(s_addr, x);
+        }
+        if (need) {
+          const float f = ex2(m_run - m_cand);      // 0 while nothing was attended yet
+          if (m_run != -INFINITY) o_scaled = true;
+          l_run *= f;
+          o_factor *= f;
+          sum_a *= f;
+          sum_b *= f;
+          m_run = m_cand;
+        }
+        const float base = (m_run == -INFINITY) ? 0.f : m_run;
+        uint32_t pk[32];
+        if (none) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = 0u;
+        } else {
+          const uint64_t sc2 = f2(sl2, sl2), nb2 = f2(-base, -base);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint64_t x = f2_fma(f2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), sc2, nb2);
+            float x0, x1;
+            f2_split(x, x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            if (c & 1) sum_b += p0 + p1;
+            else sum_a += p0 + p1;
+            pk[c] = Elem16<F16>::pack(p0, p1);
+          }
+        }
+        tmem_st32(s_addr + half * 32u, pk);
+      }
+      l_run += sum_a + sum_b;
+      if (__any_sync(0xffffffffu, o_scaled && j > j0)) {
+        // S(j) was committed behind PV(j - 1), so O is complete up to it
+        const float f = o_scaled ? o_factor : 1.f;
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c4 * 32u, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+          tmem_st32(o_addr + c4 * 32u, o);
+        }
+      }
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&bars.p_full[t]));
+    }
+    if (ok) {
+      const bool w = mbar_wait(smem_u32(&bars.fin), 0, abort_flag);
+      if (__all_sync(0xffffffffu, w) && !*abort_flag) {
+        tc_fence_after();
+        // a row whose every score was -inf is zero
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        const bool poison = *reinterpret_cast<volatile int*>(&bars.poison) != 0;
+        using T16 = typename Elem16<F16>::T;
+        T16* orow = static_cast<T16*>(p.o) + (int64_t)(c0 + i) * p.o_sn + (int64_t)h * p.o_sh;
+#pragma unroll 1
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c4 * 32u, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+          if (poison && i < n) {
+            // what the guard took out, back into this row if it attends the key
+            for (int j = j0; j < j1; ++j) {
+              if (!masked(j)) continue;
+              const int k0 = (kt_lo + j) * kKeyTile;
+              for (int u = max(k0, i - window + 1); u <= min(i, k0 + kKeyTile - 1); ++u) {
+                const uint4* vrow = reinterpret_cast<const uint4*>(
+                    static_cast<const T16*>(p.v) + (int64_t)(c0 + u) * p.v_sn + (int64_t)g * p.v_sh + c4 * 32);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const uint4 d = __ldg(vrow + x);
+                  const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) {
+                    const uint32_t bad = nonfinite_bits<F16>(wd[y]);
+                    const int at = x * 8 + y * 2;
+                    if (bad & 0x8000u) o[at] = __float_as_uint(__uint_as_float(o[at]) + Elem16<F16>::lo(wd[y]));
+                    if (bad & 0x80000000u)
+                      o[at + 1] = __float_as_uint(__uint_as_float(o[at + 1]) + Elem16<F16>::hi(wd[y]));
+                  }
+                }
+              }
+            }
+          }
+          if (i < n) {
+            uint4* dst = reinterpret_cast<uint4*>(orow + c4 * 32);
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+              uint4 w4;
+              w4.x = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 0]), __uint_as_float(o[v4 * 8 + 1]));
+              w4.y = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 2]), __uint_as_float(o[v4 * 8 + 3]));
+              w4.z = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 4]), __uint_as_float(o[v4 * 8 + 5]));
+              w4.w = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 6]), __uint_as_float(o[v4 * 8 + 7]));
+              dst[v4] = w4;
+            }
+          }
+          __syncwarp();
+        }
+        if (p.lse && i < n)
+          p.lse[(int64_t)jh * p.T + c0 + i] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+      }
+    }
+  }
+
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (tid == 0 && bars.abort) atomicExch(status, kStatusTimeout);
+}
+
+template <bool F16>
+static cudaError_t launch_typed(const PackedParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                                const CUtensorMap& tv, int* status, cudaStream_t stream) {
+  cudaError_t e =
+      cudaFuncSetAttribute(attn_packed_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  attn_packed_kernel<F16><<<(unsigned)(p.n_numbers * p.n_heads), kThreads, kSmemBytes, stream>>>(p, tq, tk, tv, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4& v, void* o, int64_t o_sn,
+                               int64_t o_sh, bool f16, int T, int Hq, int Hkv, const int32_t* heads, int n_heads,
+                               const int32_t* cu, int S, int window, float scale, float* lse, int* status,
+                               cudaStream_t stream) {
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_bnhd(&tq, q.p, 1, T, Hq, 0, q.sn, q.sh, 128) ||
+      !make_tmap_bnhd(&tk, k.p, 1, T, Hkv, 0, k.sn, k.sh, kKeyTile) ||
+      !make_tmap_bnhd(&tv, v.p, 1, T, Hkv, 0, v.sn, v.sh, kKeyTile))
+    return cudaErrorInvalidValue;
+  PackedParams p;
+  p.o = o; p.o_sn = o_sn; p.o_sh = o_sh;
+  p.v = v.p; p.v_sn = v.sn; p.v_sh = v.sh;
+  p.cu = cu; p.lse = lse;
+  p.S = S; p.T = T; p.G = Hq / Hkv; p.window = window; p.n_heads = n_heads;
+  p.n_numbers = (int64_t)T / kTileRows + S;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  for (int j = 0; j < n_heads; ++j) p.head[j] = (uint8_t)heads[j];
+  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), stream);
+  if (e != cudaSuccess) return e;
+  return f16 ? launch_typed<true>(p, tq, tk, tv, status, stream) : launch_typed<false>(p, tq, tk, tv, status, stream);
+}
+
+}  // namespace rtp

@@ -1,0 +1,662 @@
+// One new token per sequence over a paged cache, split over the cache's
+// length and joined.
+//
+// Sequence b attends the slots {0 .. sink-1} U {len-window .. len-1}, each
+// once, every head over the same set:
+//   o = sum_u p_u v_u,  p_u = exp(scale q.k_u - lse),  lse = ln sum_u exp(scale q.k_u).
+// The work is bound by HBM: 512 bytes of K and V per attended token and KV
+// head, read once for all the query heads of the group.
+//
+//   * The attended slots of a (sequence, KV head) are a segment of 64-key
+//     chunks; the segments of the whole batch form one list that the CTAs (two
+//     per SM) cut into equal runs, so that sequences of any mix of lengths
+//     load every SM alike. The lengths stay on the device: each CTA finds its
+//     run with a scan over them.
+//   * Each of a CTA's four warps owns 16 keys of every chunk: it resolves
+//     their pages one chunk ahead of the copies, copies the rows with 16-byte
+//     cp.async two chunks ahead into a private three-stage ring (zero-filled
+//     where no key is: values there cannot reach a product), and computes
+//     S = Q K^T and O += P V with mma.sync (fp32 accumulate; the heads of the
+//     group are the rows of the 16-row tile) under an online softmax. P is
+//     rounded to the cache's 16-bit type for the second product; the sum of
+//     the softmax takes it unrounded.
+//   * At the end of a segment the four warps join through shared memory. A
+//     segment that lies within one run is finished there; otherwise the CTA
+//     leaves one partial (a run has at most two: its first and its last
+//     segment), and a second kernel joins the partials of each cut segment.
+//   * With weights, the first kernel also stores the scaled scores (fp32, 4
+//     bytes against 512 / G per key and head) and a third kernel adds
+//     exp(score - lse) over the heads of a group, in a fixed order.
+#include "paged.cuh"
+
+namespace rtp {
+
+namespace {
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kCtasPerSm = 2;
+constexpr int kChunk = 64;                    // keys per chunk
+constexpr int kKeys = kChunk / kWarps;        // keys per warp and chunk
+constexpr int kStages = 3;
+constexpr int kRowBytes = RTP_D * 2;
+constexpr int kSlab = kKeys * kRowBytes;      // one warp's K (or V) rows of one chunk
+constexpr int kGroup = 16;                    // query heads per KV head: rows of the tile
+constexpr int kPart = 4 + RTP_D;              // m, l, 2 pad, o[128]
+constexpr size_t kHeaderBytes = 256;          // status word
+
+struct DecodeParams {
+  PagedView c;
+  const char* q; int64_t q_sb, q_sh;          // byte strides
+  char* o; int64_t o_sb, o_sh;
+  const int32_t* lens;
+  int B, max_len, window, sink;
+  float scale_log2;
+  int n_heads, n_ag, rows;                    // listed heads, KV heads with one, most rows of one
+  float* part;                                // [2 * CTAs, rows, kPart]
+  float* lse;                                 // caller's [B, n_heads] (natural log) or NULL
+  float* lse2;                                // [B, n_heads], log2 domain (with weights)
+  float* logits;                              // [B, n_heads, att_cap] (with weights) or NULL
+  float* w_out;
+  int64_t att_cap;                            // most attended slots of a sequence, a multiple of kChunk
+  int* status;
+  uint8_t head[kMaxHeads];                    // query heads, sorted by KV head
+  uint8_t out_row[kMaxHeads];                 // position of each in the caller's list
+  uint8_t ag_kv[kMaxHeads], ag_start[kMaxHeads], ag_n[kMaxHeads];
+};
+
+struct Smem {
+  unsigned char ring[kWarps][kStages][2][kSlab];
+  float join[2][kGroup][kPart];
+  BlockScanSmem<kThreads> scan;
+  unsigned ok[kWarps][kStages];               // which of the 16 keys are there
+  int64_t at_before;
+  int at_b, at_nc;
+};
+
+// The attended slots of one sequence: `sink` from the front, then lo .. len-1.
+struct Span {
+  int len, lo, sink, n;
+};
+__device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
+  Span s;
+  s.len = seq_len(p.lens, b, p.max_len);
+  s.lo = s.len > p.window ? s.len - p.window : 0;
+  s.sink = min(p.sink, s.lo);
+  s.n = s.sink + s.len - s.lo;
+  return s;
+}
+__device__ __forceinline__ int chunks_of(const DecodeParams& p, int b) {
+  return (span_of(p, b).n + kChunk - 1) / kChunk;
+}
+
+// Run c of a list of n chunks cut for n_ctas CTAs (n_ctas <= n).
+__device__ __forceinline__ int64_t run_start(int c, int64_t n, int n_ctas) { return (int64_t)c * n / n_ctas; }
+__device__ __forceinline__ int cta_of(int64_t x, int64_t n, int n_ctas) {
+  return (int)(((x + 1) * n_ctas - 1) / n);
+}
+
+// Chunks of the whole batch (per KV head); every thread of the block calls it.
+__device__ __forceinline__ int64_t total_chunks(const DecodeParams& p, BlockScanSmem<kThreads>& scan) {
+  int64_t all = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int tot;
+    block_exclusive_scan<kThreads>(b < p.B ? chunks_of(p, b) : 0, tot, scan);
+    all += tot;
+  }
+  return all;
+}
+// Finds the sequence that holds chunk x of the list (x < n_ag * total): its
+// number, its chunks, and the list's chunks before it.
+__device__ __forceinline__ void locate(const DecodeParams& p, int64_t x, BlockScanSmem<kThreads>& scan, int* at_b,
+                                       int* at_nc, int64_t* at_before) {
+  int64_t before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const int nc = b < p.B ? chunks_of(p, b) : 0;
+    int tot;
+    const int ex = block_exclusive_scan<kThreads>(nc, tot, scan);
+    const int64_t first = (before + ex) * p.n_ag;
+    if (nc > 0 && first <= x && x < first + (int64_t)nc * p.n_ag) {
+      *at_b = b; *at_nc = nc; *at_before = first;
+    }
+    before += tot;
+    if (before * p.n_ag > x) break;
+  }
+  __syncthreads();
+}
+
+// Walks a run: sequence-major, then KV head, then chunk.
+struct Cursor {
+  int b, a, local, nc;
+  Span s;
+  __device__ void next(const DecodeParams& p) {
+    if (++local < nc) return;
+    local = 0;
+    if (++a < p.n_ag) return;
+    a = 0;
+    do {
+      if (++b >= p.B) { b = p.B - 1; return; }           // past the last run's end
+      nc = chunks_of(p, b);
+    } while (nc == 0);
+    s = span_of(p, b);
+  }
+  // slot of key e of the segment, -1 past its end
+  __device__ int slot(int e) const { return e >= s.n ? -1 : (e < s.sink ? e : s.lo + e - s.sink); }
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+
+// Byte offset of 16-byte piece c of row r in a slab: XOR-swizzled, so that
+// the eight rows of an ldmatrix read hit distinct banks.
+__device__ __forceinline__ uint32_t slab_off(int r, int c) {
+  return (uint32_t)(r * kRowBytes + ((c ^ (r & 7)) << 4));
+}
+
+// 2^(a - b) with an empty side (-inf) weighing nothing.
+__device__ __forceinline__ float weight2(float a, float b) { return a == -INFINITY ? 0.f : exp2f(a - b); }
+
+// Writes row `j` (sorted head) of sequence b: o / l, and the log-sum-exps.
+// l == 0: nothing was attended (or every score was -inf): the row is zero.
+template <bool F16>
+__device__ __forceinline__ void write_row(const DecodeParams& p, int b, int j, float m, float l, float4 o, int lane) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint2 w;
+  w.x = Elem16<F16>::pack(o.x * inv, o.y * inv);
+  w.y = Elem16<F16>::pack(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(p.o + b * p.o_sb + (int64_t)p.head[j] * p.o_sh + lane * 8) = w;
+  if (lane == 0) {
+    const float x = l == 0.f ? -INFINITY : m + log2f(l);
+    if (p.lse2) p.lse2[(int64_t)b * p.n_heads + j] = x;
+    if (p.lse) p.lse[(int64_t)b * p.n_heads + p.out_row[j]] = x * 0.69314718055994531f;
+  }
+}
+}  // namespace
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+paged_decode_kernel(const __grid_constant__ DecodeParams p) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  pdl_wait();
+  pdl_trigger();                              // the join may launch; it waits for this grid
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gq = lane >> 2, tq = lane & 3;
+  if (blockIdx.x == 0 && tid == 0) *p.status = 0;
+  const int64_t n_list = total_chunks(p, sm.scan) * p.n_ag;
+  const int n_ctas = (int)(n_list < gridDim.x ? n_list : gridDim.x);
+  // sequences that attend nothing
+  for (int x = blockIdx.x * kWarps + warp; x < p.B * p.n_heads; x += gridDim.x * kWarps) {
+    const int b = x / p.n_heads;
+    if (chunks_of(p, b) == 0) write_row<F16>(p, b, x - b * p.n_heads, 0.f, 0.f, make_float4(0, 0, 0, 0), lane);
+  }
+  if ((int)blockIdx.x >= n_ctas) return;
+  const int64_t x0 = run_start(blockIdx.x, n_list, n_ctas);
+  const int n_t = (int)(run_start(blockIdx.x + 1, n_list, n_ctas) - x0);
+  locate(p, x0, sm.scan, &sm.at_b, &sm.at_nc, &sm.at_before);
+  Cursor cur;
+  cur.b = sm.at_b;
+  cur.nc = sm.at_nc;
+  cur.a = (int)((x0 - sm.at_before) / cur.nc);
+  cur.local = (int)((x0 - sm.at_before) - (int64_t)cur.a * cur.nc);
+  cur.s = span_of(p, cur.b);
+
+  // this warp's ring and its copies of a chunk into stage st
+  const uint32_t ring = su32(sm.ring[warp]);
+  Cursor icur = cur;                          // next chunk to copy
+  const int my_key = warp * kKeys + (lane & (kKeys - 1));
+  const int row_mask = (1 << p.c.page_shift) - 1;
+  auto fetch = [&](int& slot) -> int {        // lane r < kKeys: page of key r of the next chunk
+    slot = icur.slot(icur.local * kChunk + my_key);
+    return slot < 0 ? -1 : page_of(p.c, icur.b, slot);
+  };
+  int slot, page = fetch(slot);
+  auto issue = [&](int t) {
+    if (t < n_t) {
+      const int st = t % kStages;
+      const int g = p.ag_kv[icur.a];
+      const int64_t r64 = slot < 0 ? 0 : slot & row_mask, pg = page < 0 ? 0 : page;
+      const char* krow = p.c.k + pg * p.c.k_sp + r64 * p.c.k_sn + g * p.c.k_sh;
+      const char* vrow = p.c.v + pg * p.c.v_sp + r64 * p.c.v_sn + g * p.c.v_sh;
+      const unsigned ok = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0) sm.ok[warp][st] = ok & 0xffffu;
+      const uint32_t kdst = ring + (uint32_t)(st * 2) * kSlab, vdst = kdst + kSlab;
+      const int c = lane & 15;
+#pragma unroll
+      for (int i = 0; i < kKeys / 2; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        const char* ks = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(krow), r));
+        const char* vs = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(vrow), r));
+        const bool there = (ok >> r) & 1u;
+        cp_async16(kdst + slab_off(r, c), ks + c * 16, there);
+        cp_async16(vdst + slab_off(r, c), vs + c * 16, there);
+      }
+      if (t + 1 < n_t) {
+        icur.next(p);
+        page = fetch(slot);
+      }
+    }
+    cp_async_commit();                        // one group per chunk, empty past the run
+  };
+
+  uint32_t qa[8][4];
+  float o[16][4];
+  float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
+  int seg_local = 0;                          // first chunk of this CTA's piece of the segment
+  bool first_piece = true, fresh = true;
+
+  // Joins the warps' rows of a finished piece: warps 2, 3 into 0, 1, then 1
+  // into 0, through shared memory; warp 0 ends with the piece's sums in
+  // sm.join[0], and all warps write them out, a row at a time.
+  auto put = [&](float (*to)[kPart]) {
+    if (tq == 0) {
+      to[gq][0] = m_a; to[gq][1] = l_a;
+      to[gq + 8][0] = m_b; to[gq + 8][1] = l_b;
+    }
+#pragma unroll
+    for (int nt = 0; nt < 16; ++nt) {
+      const int col = 4 + nt * 8 + 2 * tq;
+      *reinterpret_cast<float2*>(&to[gq][col]) = make_float2(o[nt][0], o[nt][1]);
+      *reinterpret_cast<float2*>(&to[gq + 8][col]) = make_float2(o[nt][2], o[nt][3]);
+    }
+  };
+  auto add = [&](const float (*from)[kPart]) {
+    const float xa = from[gq][0], xb = from[gq + 8][0];
+    const float na = fmaxf(m_a, xa), nb = fmaxf(m_b, xb);
+    const float fa = weight2(m_a, na), fb = weight2(m_b, nb), ga = weight2(xa, na), gb = weight2(xb, nb);
+    l_a = l_a * fa + from[gq][1] * ga;
+    l_b = l_b * fb + from[gq + 8][1] * gb;
+    m_a = na; m_b = nb;
+#pragma unroll
+    for (int nt = 0; nt < 16; ++nt) {
+      const int col = 4 + nt * 8 + 2 * tq;
+      const float2 x = *reinterpret_cast<const float2*>(&from[gq][col]);
+      const float2 y = *reinterpret_cast<const float2*>(&from[gq + 8][col]);
+      o[nt][0] = o[nt][0] * fa + x.x * ga; o[nt][1] = o[nt][1] * fa + x.y * ga;
+      o[nt][2] = o[nt][2] * fb + y.x * gb; o[nt][3] = o[nt][3] * fb + y.y * gb;
+    }
+  };
+  auto finish = [&](bool whole) {
+    l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
+    l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
+    l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
+    l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
+    if (warp >= 2) put(sm.join[warp - 2]);
+    __syncthreads();
+    if (warp < 2) add(sm.join[warp]);
+    __syncthreads();
+    if (warp == 1) put(sm.join[0]);
+    __syncthreads();
+    if (warp == 0) {
+      add(sm.join[0]);
+      __syncwarp();
+      put(sm.join[0]);
+    }
+    __syncthreads();
+    const int n = p.ag_n[cur.a], j0 = p.ag_start[cur.a];
+    float* part = p.part + ((int64_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * p.rows * kPart;
+    for (int r = warp; r < n; r += kWarps) {
+      const float* row = sm.join[0][r];
+      const float4 x = *reinterpret_cast<const float4*>(row + 4 + lane * 4);
+      if (whole) {
+        write_row<F16>(p, cur.b, j0 + r, row[0], row[1], x, lane);
+      } else {
+        float* to = part + r * kPart;
+        if (lane == 0) { to[0] = row[0]; to[1] = row[1]; }
+        *reinterpret_cast<float4*>(to + 4 + lane * 4) = x;
+      }
+    }
+    __syncthreads();
+  };
+
+#pragma unroll
+  for (int t = 0; t < kStages - 1; ++t) issue(t);
+  for (int t = 0; t < n_t; ++t) {
+    issue(t + kStages - 1);
+    if (fresh) {
+      fresh = false;
+      seg_local = cur.local;
+      // query fragments (A operand, 16 x 128): row r is head ag_start + r
+      const int n = p.ag_n[cur.a], j0 = p.ag_start[cur.a];
+      const char* qb = p.q + cur.b * p.q_sb;
+      const uint32_t* qra = reinterpret_cast<const uint32_t*>(qb + (int64_t)p.head[gq < n ? j0 + gq : j0] * p.q_sh);
+      const uint32_t* qrb =
+          reinterpret_cast<const uint32_t*>(qb + (int64_t)p.head[gq + 8 < n ? j0 + gq + 8 : j0] * p.q_sh);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const int c = kk * 8 + tq;            // in pairs of elements
+        qa[kk][0] = gq < n ? __ldg(qra + c) : 0u;
+        qa[kk][1] = gq + 8 < n ? __ldg(qrb + c) : 0u;
+        qa[kk][2] = gq < n ? __ldg(qra + c + 4) : 0u;
+        qa[kk][3] = gq + 8 < n ? __ldg(qrb + c + 4) : 0u;
+      }
+      m_a = m_b = -INFINITY;
+      l_a = l_b = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < 16; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
+    }
+    cp_async_wait<kStages - 1>();             // chunk t has landed (this lane's copies)
+    __syncwarp();                             // ... and every lane's
+    const int st = t % kStages;
+    const uint32_t kbase = ring + (uint32_t)(st * 2) * kSlab, vbase = kbase + kSlab;
+    // S = Q K^T (16 rows x this warp's 16 keys)
+    float sacc[2][4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sacc[nt][e] = 0.f;
+    {
+      const int m = lane >> 3;
+      const int key = 8 * (m >> 1) + (lane & 7);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        uint32_t bf[4];
+        ldsm_x4(bf, kbase + slab_off(key, kk * 2 + (m & 1)));
+        mma16816<F16>(sacc[0], qa[kk], bf[0], bf[1]);
+        mma16816<F16>(sacc[1], qa[kk], bf[2], bf[3]);
+      }
+    }
+    // scale, mask, online softmax (rows gq and gq + 8)
+    const unsigned ok = sm.ok[warp][st];
+    float mx_a = -INFINITY, mx_b = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool there = (ok >> (nt * 8 + 2 * tq + e)) & 1u;
+        sacc[nt][e] = there ? sacc[nt][e] * p.scale_log2 : -INFINITY;
+        sacc[nt][2 + e] = there ? sacc[nt][2 + e] * p.scale_log2 : -INFINITY;
+        mx_a = fmaxf(mx_a, sacc[nt][e]);
+        mx_b = fmaxf(mx_b, sacc[nt][2 + e]);
+      }
+    if (p.logits) {
+      const int n = p.ag_n[cur.a], j0 = p.ag_start[cur.a];
+      float* at = p.logits + ((int64_t)cur.b * p.n_heads + j0) * p.att_cap + cur.local * kChunk + warp * kKeys;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        if (gq < n)
+          *reinterpret_cast<float2*>(at + gq * p.att_cap + nt * 8 + 2 * tq) = make_float2(sacc[nt][0], sacc[nt][1]);
+        if (gq + 8 < n)
+          *reinterpret_cast<float2*>(at + (gq + 8) * p.att_cap + nt * 8 + 2 * tq) =
+              make_float2(sacc[nt][2], sacc[nt][3]);
+      }
+    }
+    mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
+    mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
+    mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
+    mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 2));
+    if (mx_a > m_a || mx_b > m_b) {           // the running max only moves up: rescale O and l when it does
+      const float na = fmaxf(m_a, mx_a), nb = fmaxf(m_b, mx_b);
+      const float ra = weight2(m_a, na), rb = weight2(m_b, nb);
+      m_a = na; m_b = nb;
+      l_a *= ra; l_b *= rb;
+#pragma unroll
+      for (int nt = 0; nt < 16; ++nt) {
+        o[nt][0] *= ra; o[nt][1] *= ra;
+        o[nt][2] *= rb; o[nt][3] *= rb;
+      }
+    }
+    const float base_a = m_a == -INFINITY ? 0.f : m_a, base_b = m_b == -INFINITY ? 0.f : m_b;
+    uint32_t pa[4];                           // A fragment of P (16 rows x 16 keys)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const float e0 = exp2f(sacc[nt][0] - base_a), e1 = exp2f(sacc[nt][1] - base_a);
+      const float e2 = exp2f(sacc[nt][2] - base_b), e3 = exp2f(sacc[nt][3] - base_b);
+      l_a += e0 + e1;
+      l_b += e2 + e3;
+      pa[nt * 2 + 0] = Elem16<F16>::pack(e0, e1);
+      pa[nt * 2 + 1] = Elem16<F16>::pack(e2, e3);
+    }
+    // O += P V (16 rows x 128 dims)
+    {
+      const int m = lane >> 3;
+      const int key = 8 * (m & 1) + (lane & 7);
+#pragma unroll
+      for (int np = 0; np < 8; ++np) {
+        uint32_t bf[4];
+        ldsm_x4_t(bf, vbase + slab_off(key, 2 * np + (m >> 1)));
+        mma16816<F16>(o[2 * np], pa, bf[0], bf[1]);
+        mma16816<F16>(o[2 * np + 1], pa, bf[2], bf[3]);
+      }
+    }
+    __syncwarp();                             // stage st is free for chunk t + kStages
+    const bool seg_end = cur.local + 1 == cur.nc;
+    if (seg_end || t + 1 == n_t) {
+      finish(seg_end && seg_local == 0);
+      first_piece = false;
+      fresh = true;
+    }
+    if (t + 1 < n_t) cur.next(p);
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the partials of the segments that the runs cut: CTA (c, r) looks at
+// the boundary before run c; if that is the first one inside its segment, it
+// sums the pieces of row r in the order of the runs.
+template <bool F16>
+__global__ void __launch_bounds__(kThreads)
+paged_join_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ BlockScanSmem<kThreads> scan;
+  __shared__ int at_b, at_nc;
+  __shared__ int64_t at_before;
+  __shared__ float wm[kWarps], wl[kWarps];
+  __shared__ float4 wo[kWarps][32];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n_list = total_chunks(p, scan) * p.n_ag;
+  const int n_ctas = (int)(n_list < gridDim.x ? n_list : gridDim.x);
+  const int c = blockIdx.x;
+  if (c == 0 || c >= n_ctas) return;
+  const int64_t x = run_start(c, n_list, n_ctas);
+  locate(p, x, scan, &at_b, &at_nc, &at_before);
+  const int b = at_b, nc = at_nc;
+  const int a = (int)((x - at_before) / nc);
+  const int64_t s0 = at_before + (int64_t)a * nc;         // the segment is [s0, s0 + nc)
+  if (x == s0 || run_start(c - 1, n_list, n_ctas) > s0) return;
+  const int r = blockIdx.y;
+  if (r >= p.ag_n[a]) return;
+  const int c_last = cta_of(s0 + nc - 1, n_list, n_ctas);
+  // piece i comes from run c - 1 + i; the first is that run's last piece
+  // unless the run starts with the segment
+  const int n = c_last - (c - 1) + 1;
+  const int slot0 = (c - 1) * 2 + (run_start(c - 1, n_list, n_ctas) == s0 ? 0 : 1);
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = 8;
+  for (int i0 = warp; i0 < n; i0 += kWarps * kBatch) {
+    float ms[kBatch], ls[kBatch];
+    float4 os[kBatch];
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) {
+      const int i = i0 + s * kWarps;
+      ms[s] = -INFINITY; ls[s] = 0.f; os[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const int slot = i == 0 ? slot0 : (c - 1 + i) * 2;
+        const float* part = p.part + ((int64_t)slot * p.rows + r) * kPart;
+        ms[s] = part[0]; ls[s] = part[1];
+        os[s] = *reinterpret_cast<const float4*>(part + 4 + lane * 4);
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) top = fmaxf(top, ms[s]);
+    const float f = weight2(M, top);
+    L *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) {
+      const float wt = weight2(ms[s], top);
+      L += wt * ls[s];                        // NaN comes through, whatever its weight
+      acc.x += wt * os[s].x; acc.y += wt * os[s].y; acc.z += wt * os[s].z; acc.w += wt * os[s].w;
+    }
+    M = top;
+  }
+  if (lane == 0) { wm[warp] = M; wl[warp] = L; }
+  wo[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0) return;
+  const float top = fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3]));
+  L = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float f = weight2(wm[w], top);
+    L += f * wl[w];
+    const float4 v = wo[w][lane];
+    acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
+  }
+  write_row<F16>(p, b, p.ag_start[a] + r, top, L, acc, lane);
+}
+
+// w_out = w + sum over the group's listed heads of exp(score - lse), for
+// every slot of the sequence that is in a page.
+namespace {
+constexpr int kWeightThreads = 256;
+}
+__global__ void __launch_bounds__(kWeightThreads)
+paged_weights_kernel(const __grid_constant__ DecodeParams p) {
+  pdl_wait();
+  const int b = blockIdx.z, a = blockIdx.y;
+  const Span s = span_of(p, b);
+  const int u = blockIdx.x * kWeightThreads + threadIdx.x;
+  if (u >= s.len) return;
+  const int page = page_of(p.c, b, u);
+  if (page < 0) return;
+  const int g = p.ag_kv[a], n = p.ag_n[a], j0 = p.ag_start[a];
+  float sum = 0.f;
+  const int e = u < s.sink ? u : (u >= s.lo ? u - s.lo + s.sink : -1);
+  if (e >= 0) {
+    const float* at = p.logits + ((int64_t)b * p.n_heads + j0) * p.att_cap + e;
+    const float* lse2 = p.lse2 + (int64_t)b * p.n_heads + j0;
+    for (int r = 0; r < n; ++r) {
+      const float l2 = lse2[r];
+      sum += l2 == -INFINITY ? 0.f : exp2f(at[r * p.att_cap] - l2);
+    }
+  }
+  const int64_t w = (((int64_t)page * p.c.Hkv + g) << p.c.page_shift) + (u & ((1 << p.c.page_shift) - 1));
+  p.w_out[w] = p.c.w[w] + sum;
+}
+
+namespace {
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+int64_t attended_cap(int max_len, int window, int sink) {
+  const int64_t n = max_len <= window ? max_len : (int64_t)window + (sink < max_len - window ? sink : max_len - window);
+  return (n + kChunk - 1) / kChunk * kChunk;
+}
+constexpr int kMaxCtas = 148 * kCtasPerSm;     // partials are sized for this many
+}  // namespace
+
+size_t paged_decode_ws_bytes(int B, int max_len, int n_heads, int window, int sink, bool weights) {
+  const int rows = n_heads < kGroup ? n_heads : kGroup;
+  size_t n = kHeaderBytes + up256((size_t)2 * kMaxCtas * rows * kPart * sizeof(float));
+  if (weights)
+    n += up256((size_t)B * n_heads * sizeof(float)) +
+         (size_t)B * n_heads * attended_cap(max_len, window, sink) * sizeof(float);
+  return n;
+}
+
+template <bool F16>
+static cudaError_t launch_typed(const DecodeParams& p, int grid, cudaStream_t stream) {
+  const size_t smem = sizeof(Smem);
+  cudaError_t e =
+      cudaFuncSetAttribute(paged_decode_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_decode_kernel<F16>, dim3(grid), dim3(kThreads), smem, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_join_kernel<F16>, dim3(grid, p.rows), dim3(kThreads), 0, stream, p);
+}
+
+cudaError_t launch_paged_decode(const PagedView& c, const void* q, int64_t q_sb, int64_t q_sh, void* o, int64_t o_sb,
+                                int64_t o_sh, bool f16, int B, int G, const int32_t* heads, int n_heads,
+                                const int32_t* lens, int max_len, int window, int sink, float scale, float* lse,
+                                float* w_out, void* ws, cudaStream_t stream) {
+  DecodeParams p;
+  p.c = c;
+  p.q = static_cast<const char*>(q); p.q_sb = q_sb * 2; p.q_sh = q_sh * 2;
+  p.o = static_cast<char*>(o); p.o_sb = o_sb * 2; p.o_sh = o_sh * 2;
+  p.lens = lens; p.B = B; p.max_len = max_len; p.window = window; p.sink = sink;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.n_heads = n_heads;
+  // the listed heads, KV head by KV head
+  p.n_ag = 0; p.rows = 0;
+  int n = 0;
+  for (int g = 0; g < c.Hkv; ++g) {
+    const int start = n;
+    for (int j = 0; j < n_heads; ++j)
+      if (heads[j] / G == g) {
+        p.head[n] = (uint8_t)heads[j];
+        p.out_row[n++] = (uint8_t)j;
+      }
+    if (n == start) continue;
+    p.ag_kv[p.n_ag] = (uint8_t)g;
+    p.ag_start[p.n_ag] = (uint8_t)start;
+    p.ag_n[p.n_ag] = (uint8_t)(n - start);
+    ++p.n_ag;
+    if (n - start > p.rows) p.rows = n - start;
+  }
+  if (p.rows > kGroup) return cudaErrorInvalidValue;
+  p.lse = lse;
+  p.w_out = w_out;
+  p.att_cap = attended_cap(max_len, window, sink);
+  char* base = static_cast<char*>(ws);
+  p.status = reinterpret_cast<int*>(base);
+  p.part = reinterpret_cast<float*>(base + kHeaderBytes);
+  p.lse2 = nullptr;
+  p.logits = nullptr;
+  if (w_out) {
+    const int most_rows = n_heads < kGroup ? n_heads : kGroup;
+    char* at = base + kHeaderBytes + up256((size_t)2 * kMaxCtas * most_rows * kPart * sizeof(float));
+    p.lse2 = reinterpret_cast<float*>(at);
+    p.logits = reinterpret_cast<float*>(at + up256((size_t)B * n_heads * sizeof(float)));
+  }
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  int64_t grid = (int64_t)B * p.n_ag * (p.att_cap / kChunk);
+  const int most = sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
+  if (grid > most) grid = most;
+  e = f16 ? launch_typed<true>(p, (int)grid, stream) : launch_typed<false>(p, (int)grid, stream);
+  if (e != cudaSuccess) return e;
+  if (w_out) {
+    const dim3 g((max_len + kWeightThreads - 1) / kWeightThreads, p.n_ag, B);
+    e = launch_pdl(paged_weights_kernel, g, dim3(kWeightThreads), 0, stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace rtp

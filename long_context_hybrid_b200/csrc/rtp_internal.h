@@ -141,6 +141,43 @@ cudaError_t launch_select_prefill_tc(const void* qt, const void* kt, int64_t kt_
                                      const int32_t* kv_of, int topk, int32_t* blocks, int32_t* counts,
                                      int* status, cudaStream_t stream);
 
+// ---------------------------------------------------------------------------
+// Serving: packed prompts and the paged cache
+// ---------------------------------------------------------------------------
+// A paged cache as the kernels see it: byte strides, 16-bit elements; slot s
+// of sequence b is row s % page_size of page table[b][s / page_size].
+struct PagedView {
+  char* k; int64_t k_sp, k_sn, k_sh;      // page, row, head strides (bytes)
+  char* v; int64_t v_sp, v_sn, v_sh;
+  float* w;                               // [num_pages, Hkv, page_size], may be NULL
+  const int32_t* table; int64_t table_stride;
+  int64_t capacity;                       // slots of a table row: max_pages * page_size
+  int num_pages, page_shift, Hkv;
+};
+
+cudaError_t launch_paged_append(const PagedView& c, const void* k, int64_t k_sn, int64_t k_sh, const void* v,
+                                int64_t v_sn, int64_t v_sh, const float* w, const int32_t* cu, const int32_t* pos,
+                                int S, int T, cudaStream_t stream);
+cudaError_t launch_cache_evict(const PagedView& src, const PagedView& dst, bool in_place, int B,
+                               const int32_t* lens, int max_len, int budget, int sink, int recent, int32_t* idx,
+                               int32_t* new_lens, cudaStream_t stream);
+
+// One new token per sequence over the paged cache; heads sorted by KV head.
+size_t paged_decode_ws_bytes(int B, int max_len, int n_heads, int window, int sink, bool weights);
+cudaError_t launch_paged_decode(const PagedView& c, const void* q, int64_t q_sb, int64_t q_sh, void* o, int64_t o_sb,
+                                int64_t o_sh, bool f16, int B, int G, const int32_t* heads, int n_heads,
+                                const int32_t* lens, int max_len, int window, int sink, float scale, float* lse,
+                                float* w_out, void* ws, cudaStream_t stream);
+
+// Causal attention of packed prompts, and the attention weight each key got.
+cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4& v, void* o, int64_t o_sn,
+                               int64_t o_sh, bool f16, int T, int Hq, int Hkv, const int32_t* heads, int n_heads,
+                               const int32_t* cu, int S, int window, float scale, float* lse, int* status,
+                               cudaStream_t stream);
+cudaError_t launch_key_weights(const Tensor4& q, const Tensor4& k, bool f16, int T, int Hq, int Hkv,
+                               const int32_t* heads, int n_heads, const int32_t* cu, int S, const float* lse,
+                               int n_obs, int window, float scale, float* weights, int* status, cudaStream_t stream);
+
 // Bytes of the status word every prefill attention call keeps in its workspace.
 constexpr size_t kStatusBytes = 256;
 
