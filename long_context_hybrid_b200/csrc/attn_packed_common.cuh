@@ -24,48 +24,186 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ float max3f(float a, float b, float c) {
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Maximum of three, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// mbar_wait without the suspend-time hint: woken sooner (a step of the packed
+// attention takes 3950 clocks with it, 4300 with the hint), and the few warps
+// that wait here take few issue slots. Bounded alike.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_test(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// The same for the MMA warps: on running out it only raises the flag. The
+// warp then goes on through its loop (every later wait returns at once, its
+// products read and write on-chip memory only, and nothing is stored), which
+// keeps its control flow uniform and with it the descriptors in uniform
+// registers.
+// The whole warp calls it and leaves it together: a lane left behind at a
+// barrier could find it a full turn further on, and wait for good.
+__device__ __forceinline__ void mbar_pass(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (!mbar_test(bar, parity)) {
+    const long long t0 = clock64();
+    for (uint32_t it = 1; !mbar_test(bar, parity); ++it) {
+      if ((it & 63u) == 0) {
+        if (*abort_flag) break;
+        if (clock64() - t0 > kWaitLimitCycles) {
+          *abort_flag = 1;
+          break;
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// 2^x of a pair on the fp32 pipe, for x <= 127 (smaller than -126: 2^-126):
+// x = n + f with n the nearest integer (added and subtracted 1.5 * 2^23, whose
+// sum also holds n in its low bits), 2^f by a polynomial, n added to the
+// exponent. The polynomial is the degree-4 minimax fit to 2^f in relative error on
+// [-1/2, 1/2] (Remez exchange): off by at most 2.7e-6, 4e-8 in the mean.
+__device__ __forceinline__ uint64_t f2_ex2(uint64_t x) {
+  float x0, x1;
+  f2_split(x, x0, x1);
+  const uint64_t xc = f2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const uint64_t big = f2(12582912.f, 12582912.f), neg_big = f2(-12582912.f, -12582912.f);
+  const uint64_t r = f2_add(xc, big);
+  const uint64_t f = f2_fma(f2_add(r, neg_big), f2(-1.f, -1.f), xc);
+  uint64_t y = f2_fma(f, f2(0.00957010221f, 0.00957010221f), f2(0.0559178591f, 0.0559178591f));
+  y = f2_fma(y, f, f2(0.240247443f, 0.240247443f));
+  y = f2_fma(y, f, f2(0.693121791f, 0.693121791f));
+  y = f2_fma(y, f, f2(0.999999285f, 0.999999285f));
+  float r0, r1, y0, y1;
+  f2_split(r, r0, r1);
+  f2_split(y, y0, y1);
+  return f2(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23)),
+            __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23)));
+}
+
 __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity))
     if (clock64() - t0 > 200000000LL) return false;
   return true;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// The MMA warp runs its loop with all 32 lanes and issues under the predicate
+// of one elected lane: descriptors then stay in uniform registers. Inside a
+// branch of a single thread every operand takes a detour (measured: 115 clocks
+// from one 128 x 128 x 16 product to the next, which itself takes 64).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(bar), "r"(on)
       : "memory");
 }
 // Both operands are of the one input type: bf16, or f16 (format code 0).
-template <bool F16>
+template <bool F16, int N = 128>
 __host__ __device__ constexpr uint32_t idesc(bool b_mn_major) {
-  return idesc_bf16_f32(128, 128, false, b_mn_major) & (F16 ? ~((7u << 7) | (7u << 10)) : ~0u);
+  return idesc_bf16_f32(128, N, false, b_mn_major) & (F16 ? ~((7u << 7) | (7u << 10)) : ~0u);
 }
-// D = A B^T of two K-major 128 x 128 tiles (8 K-steps of 16 over D = 128).
-template <bool F16>
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_smem, uint32_t k_smem) {
+// Descriptors of 128 x 128 tiles: K-major (Q, K) and MN-major (V); a tile
+// `bytes` further on is + (bytes >> 4).
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr) { return desc_sw128(saddr, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr) { return desc_sw128(saddr, 16384, 1024); }
+
+// D = A B^T of two K-major tiles, N rows of B (8 K-steps of 16 over D = 128).
+template <bool F16, int N = 128>
+__device__ __forceinline__ void issue_qk(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc) {
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t off = (kk >> 2) * 16384u + (kk & 3) * 32u;
-    mma_bf16_ss(d_tmem, desc_sw128(q_smem + off, 16, 1024), desc_sw128(k_smem + off, 16, 1024), idesc<F16>(false),
-                kk > 0 ? 1u : 0u);
+    const uint64_t off = ((kk >> 2) * 16384u + (kk & 3) * 32u) >> 4;
+    mma_ss_if(on, d_tmem, a_desc + off, b_desc + off, idesc<F16, N>(false), kk > 0 ? 1u : 0u);
   }
 }
-// D (+)= P V: P in TMEM (8 K-steps of 16 keys = 8 columns each), V MN-major.
+// D (+)= P V over the 64 keys of one half of a V tile (MN-major): P in TMEM (4
+// K-steps of 16 keys = 8 columns each).
 template <bool F16>
-__device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t v_smem, bool accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t on, uint32_t o_tmem, uint32_t p_tmem, uint64_t v_desc, int half,
+                                         bool accumulate) {
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_ts(o_tmem, p_tmem + kk * 8u, desc_sw128(v_smem + kk * 2048u, 16384, 1024), idesc<F16>(true),
-           (accumulate || kk > 0) ? 1u : 0u);
+  for (int k = 0; k < 4; ++k) {
+    const int kk = half * 4 + k;
+    mma_ts_if(on, o_tmem, p_tmem + k * 8u, v_desc + ((kk * 2048u) >> 4), idesc<F16>(true),
+              (accumulate || k > 0) ? 1u : 0u);
+  }
 }
 
 }  // namespace sm100

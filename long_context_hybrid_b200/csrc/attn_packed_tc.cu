@@ -16,9 +16,11 @@
 //              128-byte swizzle) through a ring of five: a stage holds either, so
 //              the ring is two and a half key tiles deep beside 64 KB of Q;
 //   warp 1     TMEM owner and MMA issuer: S_t = Q_t K^T (M128 N128 K128) and
-//              O_t += P_t V (P from TMEM, V MN-major), in the order
-//              PV0 QK0' PV1 QK1', so that one tile's products run under the
-//              other's softmax; a query tile takes only the key tiles that it attends;
+//              O_t += P_t V (P from TMEM, where it takes the place of S; V
+//              MN-major) in the order PV0 QK0' PV1 QK1', so that one query
+//              tile's products run under the other's softmax. The product with
+//              a tile's first 64 keys starts while the softmax works on the
+//              other 64. A query tile takes only the key tiles that it attends;
 //   warps 2, 3 V guard: in key tiles that a mask cuts, rows behind the sequence's
 //              end and non-finite values are zeroed before the product (there
 //              P is 0, and 0 * NaN would reach rows that do not attend the
@@ -30,6 +32,8 @@
 //              range of both 16-bit types), row sum in fp32 from the
 //              unrounded exponentials, P rounded to the input type over S in TMEM.
 // Every wait is bounded, as in the other tensor-core kernels.
+#include <type_traits>
+
 #include "attn_packed_common.cuh"
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -47,6 +51,10 @@ constexpr uint32_t kStage = 32768;                   // one K or V tile: [D half
 constexpr uint32_t kRingOff = 2 * kStage;            // behind the two Q tiles
 constexpr uint32_t kTmemCols = 512;                  // tile t: S at 256 t, O at 256 t + 128
 constexpr int kStatusTimeout = 4;
+// Every kPolyEvery-th pair of exponentials of an uncut tile goes to the fp32
+// pipe instead of the exponential unit (16 a clock and SM: 1024 clocks a tile of
+// 128 x 128, as long as its two products).
+constexpr int kPolyEvery = 8;
 
 struct PackedParams {
   void* o; int64_t o_sn, o_sh;
@@ -61,7 +69,7 @@ struct PackedParams {
 
 struct Bars {
   uint64_t q_full[2], full[kRing], empty[kRing], v_ok[kRing];
-  uint64_t s_full[2], p_full[2], fin;
+  uint64_t s_full[2], p_full[2][2], fin;             // p_full[query tile][64-key half]
   uint32_t tmem_base;
   int abort;
   int poison;                                        // the guard met a non-finite value of the sequence
@@ -91,10 +99,12 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
   const int jh = blockIdx.x % p.n_heads;
   const int h = p.head[jh], g = h / p.G;
   int c0, n, row0;                                   // the sequence's first row and length, the CTA's first row in it
+  // a wait runs out seconds after its block began, long after this
+  if (blockIdx.x == 0 && tid == 0) *status = 0;
   if (!packed_tile(p.cu, p.S, p.T, kTileRows, p.n_numbers - 1 - blockIdx.x / p.n_heads, &c0, &n, &row0)) return;
 
   // key tiles kt_lo .. kt_lo + n_tiles - 1 (of 128 keys); query tile t takes
-  // those of [first[t], last[t])
+  // those of [first[t], last[t]), counted from kt_lo
   const int window = p.window;
   int first[2], last[2];
   const int kt_lo = max(0, row0 - window + 1) / kKeyTile;
@@ -117,7 +127,7 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&bars.q_full[t]), 1);
       mbar_init(smem_u32(&bars.s_full[t]), 1);
-      mbar_init(smem_u32(&bars.p_full[t]), 128);
+      for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&bars.p_full[t][x]), 4);
     }
     for (int s = 0; s < kRing; ++s) {
       mbar_init(smem_u32(&bars.full[s]), 1);
@@ -136,9 +146,12 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars.tmem_base;
-
-  if (warp == 0) {
+  constexpr uint32_t tmem = 0;                       // every column is allocated, so the address is 0
+  // 128 * (80 + 2 * 208) registers of the launch's 384 * 168: a softmax thread
+  // holds its row of 128 scores
+  if (warp < 4) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       tma_prefetch(&tmQ);
@@ -178,47 +191,60 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
           wait_short(smem_u32(&bars.full[r % kRing]), (r / kRing) & 1);
       }
     }
-  } else if (warp == 1) {
+   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = true;
-      auto full = [&](int r) { return mbar_wait(smem_u32(&bars.full[r % kRing]), (r / kRing) & 1, abort_flag); };
-      for (int j = -1; ok && j < n_tiles; ++j) {
-        const int kr = 2 * (j + 1), vr = 2 * j + 1;
-        const uint32_t k_s = sb + kRingOff + (uint32_t)(kr % kRing) * kStage;
-        const uint32_t v_s = sb + kRingOff + (uint32_t)((vr + kRing) % kRing) * kStage;
+    const uint32_t on = elect_one();
+    const uint64_t q_desc = desc_k_major(sb), k_desc = desc_k_major(sb + kRingOff),
+                   v_desc = desc_mn_major(sb + kRingOff);
+    // stage and turn of the K and V item in use
+    int k_st = 0, k_turn = 0, v_st = 1, v_turn = 0;
+    for (int j = -1; j < n_tiles; ++j) {
+      const uint64_t v_d = v_desc + (uint64_t)v_st * (kStage >> 4);
+      const uint64_t k_d = k_desc + (uint64_t)k_st * (kStage >> 4);
+      if (j >= 0) {
+        mbar_pass(smem_u32(&bars.full[v_st]), v_turn & 1, abort_flag);
+        mbar_pass(smem_u32(&bars.v_ok[v_st]), (v_turn >> 1) & 1, abort_flag);
+      }
+      if (j + 1 < n_tiles) mbar_pass(smem_u32(&bars.full[k_st]), k_turn & 1, abort_flag);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j >= first[t] && j < last[t]) {
-            // v_ok of every tile, so that the guard never falls a ring behind
-            ok = ok && mbar_wait(smem_u32(&bars.p_full[t]), (j - first[t]) & 1, abort_flag) && full(vr) &&
-                 mbar_wait(smem_u32(&bars.v_ok[vr % kRing]), (vr / (2 * kRing)) & 1, abort_flag);
-            if (!ok) break;
+      for (int t = 0; t < 2; ++t) {
+        if (j >= first[t] && j < last[t]) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            mbar_pass(smem_u32(&bars.p_full[t][half]), (j - first[t]) & 1, abort_flag);
             tc_fence_after();
-            issue_pv<F16>(tmem + t * 256u + 128u, tmem + t * 256u, v_s, j > first[t]);
+            issue_pv<F16>(on, t * 256u + 128u, t * 256u + half * 32u, v_d, half, half || j > first[t]);
           }
-          if (t == 1 && j >= 0) mma_commit(smem_u32(&bars.empty[vr % kRing]));
-          if (j + 1 >= first[t] && j + 1 < last[t]) {
-            ok = ok && (j + 1 > first[t] || mbar_wait(smem_u32(&bars.q_full[t]), 0, abort_flag)) && full(kr);
-            if (!ok) break;
-            tc_fence_after();
-            issue_qk<F16>(tmem + t * 256u, sb + t * kStage, k_s);
-            mma_commit(smem_u32(&bars.s_full[t]));
-          }
-          if (t == 1 && j + 1 < n_tiles) mma_commit(smem_u32(&bars.empty[kr % kRing]));
+        }
+        if (j + 1 >= first[t] && j + 1 < last[t]) {
+          if (j + 1 == first[t]) mbar_pass(smem_u32(&bars.q_full[t]), 0, abort_flag);
+          tc_fence_after();
+          issue_qk<F16>(on, t * 256u, q_desc + t * (kStage >> 4), k_d);
+          commit_if(on, smem_u32(&bars.s_full[t]));
         }
       }
-      mma_commit(smem_u32(&bars.fin));
-      wait_short(smem_u32(&bars.fin), 0);
+      if (j >= 0) {
+        commit_if(on, smem_u32(&bars.empty[v_st]));
+        v_st += 2;
+        if (v_st >= kRing) { v_st -= kRing; ++v_turn; }
+      }
+      if (j + 1 < n_tiles) commit_if(on, smem_u32(&bars.empty[k_st]));
+      k_st += 2;
+      if (k_st >= kRing) { k_st -= kRing; ++k_turn; }
     }
+    commit_if(on, smem_u32(&bars.fin));
+    wait_short(smem_u32(&bars.fin), 0);
     __syncwarp();
-  } else if (warp < 4) {
+   } else {
     // ------------------------------------------------------------ V guard
     const int gt = tid - 64;
-    for (int j = 0; j < n_tiles; ++j) {
-      const int r = 2 * j + 1, s = r % kRing;
-      const bool w = mbar_wait(smem_u32(&bars.full[s]), (r / kRing) & 1, abort_flag);
+    for (int r = 0; r < 2 * n_tiles; ++r) {
+      // K items are waited for too: copies may complete out of order, and a
+      // wait that skips a turn of a stage could not tell it from the last one
+      const int s = r % kRing, j = r >> 1;
+      const bool w = mbar_spin(smem_u32(&bars.full[s]), (r / kRing) & 1, abort_flag);
       if (!__all_sync(0xffffffffu, w)) break;
+      if (!(r & 1)) continue;
       if (masked(j)) {
         uint4* tile = reinterpret_cast<uint4*>(smem + kRingOff + s * kStage);
         const int there = n - (kt_lo + j) * kKeyTile;     // rows of the tile that are keys of the sequence
@@ -241,7 +267,9 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
       }
       if (lane == 0) mbar_arrive(smem_u32(&bars.v_ok[s]));
     }
+   }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax
     const int t = (warp - 4) >> 2;                  // query tile of this warpgroup
     const int r = (warp & 3) * 32 + lane;           // row within the tile = TMEM lane
@@ -250,100 +278,95 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     const float sl2 = p.scale_log2;
     const uint32_t s_addr = tmem + lane_off + t * 256u, o_addr = s_addr + 128u;
     const int j0 = first[t], j1 = last[t];
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = -INFINITY;
+    uint64_t sum = 0;                               // the row's sum, even and odd keys
+    const uint64_t sc2 = f2(sl2, sl2);
     bool ok = j1 > j0;
     for (int j = j0; j < j1; ++j) {
-      const bool w = mbar_wait(smem_u32(&bars.s_full[t]), (j - j0) & 1, abort_flag);
+      const bool w = mbar_spin(smem_u32(&bars.s_full[t]), (j - j0) & 1, abort_flag);
       if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
       tc_fence_after();
-      // Each 64-key half: mask, a lazy update of the maximum, exponentials, and
-      // P written as 16-bit pairs over S columns [32 half, 32 half + 32). If the
-      // second half raises the maximum by more than 8, the first half's P is
-      // rescaled in TMEM.
-      float o_factor = 1.f;
-      bool o_scaled = false;
-      float sum_a = 0.f, sum_b = 0.f;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int key0 = (kt_lo + j) * kKeyTile + half * 64;
-        const bool none = key0 > i || key0 + 63 <= i - window;
-        const bool all = key0 + 63 <= i && key0 > i - window;
-        uint32_t v[64];
-        tmem_ld32(s_addr + half * 64u, v);
-        tmem_ld32(s_addr + half * 64u + 32u, v + 32);
+      const int key0 = (kt_lo + j) * kKeyTile;
+      auto tile = [&](auto is_cut) {
+        constexpr bool kCut = decltype(is_cut)::value;
+        uint32_t v[128];
+        tmem_ld32(s_addr, v);
+        tmem_ld32(s_addr + 32u, v + 32);
         tc_wait_ld();
-        if (!none && !all) {
+        tmem_ld32(s_addr + 64u, v + 64);             // under the first half's maximum
+        tmem_ld32(s_addr + 96u, v + 96);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (key0 + c > i || key0 + c <= i - window) v[c] = __float_as_uint(-INFINITY);
-        }
-        float mx = -INFINITY;
-        if (!none) {
-          float a0 = -INFINITY, a1 = -INFINITY;
+        for (int half = 0; half < 2; ++half) {
+          if (half) tc_wait_ld();
+          if (kCut) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            a0 = max3f(a0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-            a1 = max3f(a1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+            for (int c = half * 64; c < half * 64 + 64; ++c)
+              if (key0 + c > i || key0 + c <= i - window) v[c] = __float_as_uint(-INFINITY);
           }
-          mx = fmaxf(a0, a1);
+#pragma unroll
+          for (int c = half * 64; c < half * 64 + 64; c += 2)
+            top[(c >> 1) & 3] =
+                max3_nan(top[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
         }
-        const float m_cand = mx * sl2;
+        const float m_cand = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]) * sl2;
+        // a NaN or +inf among the scores makes the whole row NaN
+        if (!(m_cand < INFINITY)) sum = f2(NAN, NAN);
         const bool need = m_cand > m_run + 8.f;
-        if (half == 1 && __any_sync(0xffffffffu, need && m_run != -INFINITY)) {
-          const float f = (need && m_run != -INFINITY) ? ex2(m_run - m_cand) : 1.f;
-          uint32_t x[32];
-          tmem_ld32(s_addr, x);
-          tc_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = Elem16<F16>::pack(Elem16<F16>::lo(x[c]) * f, Elem16<F16>::hi(x[c]) * f);
-          tmem_st32(s_addr, x);
-        }
-        if (need) {
-          const float f = ex2(m_run - m_cand);      // 0 while nothing was attended yet
-          if (m_run != -INFINITY) o_scaled = true;
-          l_run *= f;
-          o_factor *= f;
-          sum_a *= f;
-          sum_b *= f;
-          m_run = m_cand;
-        }
+        const float f = need ? ex2(m_run - m_cand) : 1.f;     // 0 while nothing was attended yet
+        if (need) m_run = m_cand;
+        const bool rescale = __any_sync(0xffffffffu, need) && j > j0;
+        sum = f2_mul(sum, f2(f, f));
         const float base = (m_run == -INFINITY) ? 0.f : m_run;
-        uint32_t pk[32];
-        if (none) {
+        const uint64_t nb2 = f2(-base, -base);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) pk[c] = 0u;
-        } else {
-          const uint64_t sc2 = f2(sl2, sl2), nb2 = f2(-base, -base);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const uint64_t x = f2_fma(f2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), sc2, nb2);
-            float x0, x1;
-            f2_split(x, x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            if (c & 1) sum_b += p0 + p1;
-            else sum_a += p0 + p1;
+            const int at = half * 64 + 2 * c;
+            const uint64_t x = f2_fma(f2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), sc2, nb2);
+            float p0, p1;
+            if (!kCut && c % kPolyEvery == kPolyEvery - 1) {
+              f2_split(f2_ex2(x), p0, p1);
+            } else {
+              float x0, x1;
+              f2_split(x, x0, x1);
+              p0 = ex2(x0);
+              p1 = ex2(x1);
+            }
+            sum = f2_add(sum, f2(p0, p1));
             pk[c] = Elem16<F16>::pack(p0, p1);
           }
-        }
-        tmem_st32(s_addr + half * 32u, pk);
-      }
-      l_run += sum_a + sum_b;
-      if (__any_sync(0xffffffffu, o_scaled && j > j0)) {
-        // S(j) was committed behind PV(j - 1), so O is complete up to it
-        const float f = o_scaled ? o_factor : 1.f;
+          tmem_st32(s_addr + half * 32u, pk);
+          if (half == 0 && rescale) {
+            // S(j) was committed behind PV(j - 1), so O is complete up to it
+#pragma unroll 1
+            for (int c8 = 0; c8 < 8; ++c8) {
+              uint32_t o[16];
+              tmem_ld16(o_addr + c8 * 16u, o);
+              tc_wait_ld();
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + c4 * 32u, o);
-          tc_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-          tmem_st32(o_addr + c4 * 32u, o);
+              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+              tmem_st16(o_addr + c8 * 16u, o);
+            }
+          }
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[t][half]));
         }
-      }
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&bars.p_full[t]));
+      };
+      // two copies: with the mask as selects every tile would pay for it
+      const bool cut = __any_sync(0xffffffffu, key0 + kKeyTile - 1 > i || key0 <= i - window);
+      if (cut) tile(std::true_type{});
+      else tile(std::false_type{});
+    }
+    float l_run;
+    {
+      float s0, s1;
+      f2_split(sum, s0, s1);
+      l_run = s0 + s1;
     }
     if (ok) {
       const bool w = mbar_wait(smem_u32(&bars.fin), 0, abort_flag);
@@ -442,8 +465,6 @@ cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4
   p.n_numbers = (int64_t)T / kTileRows + S;
   p.scale_log2 = scale * 1.4426950408889634f;
   for (int j = 0; j < n_heads; ++j) p.head[j] = (uint8_t)heads[j];
-  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), stream);
-  if (e != cudaSuccess) return e;
   return f16 ? launch_typed<true>(p, tq, tk, tv, status, stream) : launch_typed<false>(p, tq, tk, tv, status, stream);
 }
 

@@ -23,6 +23,7 @@
 // buffers), warps 4-7 and 8-11 two warpgroups that take the tiles in turn.
 #include <cooperative_groups.h>
 #include <stddef.h>
+#include <type_traits>
 
 #include "attn_packed_common.cuh"
 #include "paged.cuh"
@@ -58,7 +59,7 @@ struct Shared {
   uint64_t k_full, full[kRing], empty[kRing], s_full[kBufs], s_empty[kBufs], fin;
   uint32_t tmem_base;
   int abort;
-  __align__(16) float neg_lse[2][2][kTile];          // [warpgroup][parity][column], log2 domain; read 16 bytes at a time
+  __align__(16) float neg_lse[8][kTile];             // [warp][column], log2 domain; read 16 bytes at a time
   float sum[2][kTile];                               // per warpgroup, read by the cluster
 };
 static_assert(offsetof(Shared, neg_lse) % 16 == 0, "16-byte reads");
@@ -82,6 +83,8 @@ key_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant
   const int unit = blockIdx.x / n_ranks;
   const int a = unit % p.n_ag, g = p.ag_kv[a];
   int c0, n, k0;
+  // a wait runs out seconds after its block began, long after this
+  if (blockIdx.x == 0 && tid == 0) *status = 0;
   if (!packed_tile(p.cu, p.S, p.T, kTile, unit / p.n_ag, &c0, &n, &k0)) return;   // the whole cluster alike
 
   // query rows that attend a key of the tile: [q_lo, q_hi), in tiles of 128
@@ -102,7 +105,7 @@ key_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant
     }
     for (int s = 0; s < kBufs; ++s) {
       mbar_init(smem_u32(&sh.s_full[s]), 1);
-      mbar_init(smem_u32(&sh.s_empty[s]), 128);
+      mbar_init(smem_u32(&sh.s_empty[s]), 4);
     }
     mbar_init(smem_u32(&sh.fin), 1);
     sh.abort = 0;
@@ -150,19 +153,22 @@ key_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n_x > 0) {
+    if (n_x > 0) {
+      const uint32_t on = elect_one();
+      const uint64_t k_desc = desc_k_major(sb), q_desc = desc_k_major(sb + kRingOff);
       bool ok = mbar_wait(smem_u32(&sh.k_full), 0, abort_flag);
       for (int i = 0; ok && i < n_x; ++i) {
         const int s = i % kRing, buf = i % kBufs;
         ok = mbar_wait(smem_u32(&sh.full[s]), (i / kRing) & 1, abort_flag) &&
              (i < kBufs || mbar_wait(smem_u32(&sh.s_empty[buf]), (i / kBufs - 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        issue_qk<F16>(tmem + buf * 128u, sb, sb + kRingOff + s * kStage);
-        mma_commit(smem_u32(&sh.s_full[buf]));
-        mma_commit(smem_u32(&sh.empty[s]));
+        issue_qk<F16>(on, tmem + buf * 128u, k_desc, q_desc + (uint64_t)s * (kStage >> 4));
+        commit_if(on, smem_u32(&sh.s_full[buf]));
+        commit_if(on, smem_u32(&sh.empty[s]));
       }
-      mma_commit(smem_u32(&sh.fin));
+      commit_if(on, smem_u32(&sh.fin));
       wait_short(smem_u32(&sh.fin), 0);
     }
     __syncwarp();
@@ -173,63 +179,76 @@ key_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int u = k0 + r;
     const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-    // column c of tile i: -lse in the log2 domain; a row that attended nothing weighs nothing
-    auto fetch = [&](int i) -> float {
+    // Each warp keeps its own copy of a tile's -lse (log2 domain), fetched one
+    // tile ahead: lane l holds columns l, l + 32, .. A row that attended nothing
+    // weighs nothing.
+    float* nl = sh.neg_lse[warp - 4];
+    float next[4];
+    auto fetch = [&](int i) {
       const int x = rank + i * n_ranks;
-      const int row = (t_lo + x % n_q) * kTile + r;
-      if (i >= n_x || row >= n) return -INFINITY;
-      const float l = __ldg(p.lse + (int64_t)p.lse_row[p.ag_start[a] + x / n_q] * p.T + c0 + row);
-      return l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+      const int hh = x / n_q, row0 = (t_lo + x - hh * n_q) * kTile;
+      const float* from = p.lse + (int64_t)p.lse_row[p.ag_start[a] + hh] * p.T + c0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int row = row0 + y * 32 + lane;
+        const float l = row < n ? __ldg(from + row) : -INFINITY;
+        next[y] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+      }
     };
     float total = 0.f;
-    bool ok = true;              // after a wait that ran out a warp still meets the others at every barrier
-    float next = n_x > wg ? fetch(wg) : 0.f;
+    if (n_x > wg) fetch(wg);
     for (int i = wg; i < n_x; i += 2) {
-      const int buf = i % kBufs, par = (i >> 1) & 1;
-      float* nl = sh.neg_lse[wg][par];
-      nl[r] = next;
-      asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
-      next = fetch(i + 2);
+      const int buf = i % kBufs;
+      __syncwarp();
+#pragma unroll
+      for (int y = 0; y < 4; ++y) nl[y * 32 + lane] = next[y];
+      __syncwarp();
+      if (i + 2 < n_x) fetch(i + 2);
       const int x = rank + i * n_ranks;
       const int q0 = (t_lo + x % n_q) * kTile;
-      const bool w = ok && mbar_wait(smem_u32(&sh.s_full[buf]), (i / kBufs) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, w);
-      if (!ok) continue;
+      const bool w = mbar_wait(smem_u32(&sh.s_full[buf]), (i / kBufs) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, w)) break;
       tc_fence_after();
       // some pair of the tile is masked: a query before the tile's last key, not
       // observed or past the end, or a key out of a query's window
       const bool cut = q0 < k0 + kTile - 1 || q0 < obs0 || q0 + kTile > n ||
                        (int64_t)q0 + kTile - 1 - k0 >= p.window;
-      const int64_t c_hi64 = (int64_t)u + p.window - q0;
-      const int c_lo = max(u, obs0) - q0, c_hi = (int)min((int64_t)(n - q0), c_hi64);   // columns [c_lo, c_hi)
+      const int c_lo = max(u, obs0) - q0;
+      const int c_hi = (int)min((int64_t)(n - q0), (int64_t)u + p.window - q0);   // columns [c_lo, c_hi)
       uint64_t acc0 = 0, acc1 = 0;                   // pairs of +0
+      auto add_tile = [&](auto is_cut) {
 #pragma unroll
-      for (int c4 = 0; c4 < 4; ++c4) {
-        uint32_t v[32];
-        tmem_ld32(tmem + lane_off + buf * 128u + c4 * 32u, v);
-        tc_wait_ld();
-        if (c4 == 3) {
-          tc_fence_before();
-          mbar_arrive(smem_u32(&sh.s_empty[buf]));
-        }
-        const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(nl + c4 * 32);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const ulonglong2 l = nl2[c];
-          float e0, e1, e2, e3;
-          f2_split(f2_fma(f2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), sc2, l.x), e0, e1);
-          f2_split(f2_fma(f2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), sc2, l.y), e2, e3);
-          if (cut) {
-            const int col = c4 * 32 + 4 * c;
-            if (col < c_lo || col >= c_hi) e0 = -INFINITY;
-            if (col + 1 < c_lo || col + 1 >= c_hi) e1 = -INFINITY;
-            if (col + 2 < c_lo || col + 2 >= c_hi) e2 = -INFINITY;
-            if (col + 3 < c_lo || col + 3 >= c_hi) e3 = -INFINITY;
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_off + buf * 128u + c4 * 32u, v);
+          tc_wait_ld();
+          if (c4 == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.s_empty[buf]));
           }
-          acc0 = f2_add(acc0, f2(ex2(e0), ex2(e1)));
-          acc1 = f2_add(acc1, f2(ex2(e2), ex2(e3)));
+          const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(nl + c4 * 32);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const ulonglong2 l = nl2[c];
+            float e[4];
+            f2_split(f2_fma(f2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), sc2, l.x), e[0], e[1]);
+            f2_split(f2_fma(f2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), sc2, l.y), e[2], e[3]);
+            if constexpr (decltype(is_cut)::value) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int col = c4 * 32 + 4 * c + y;
+                if (col < c_lo || col >= c_hi) e[y] = -INFINITY;
+              }
+            }
+            acc0 = f2_add(acc0, f2(ex2(e[0]), ex2(e[1])));
+            acc1 = f2_add(acc1, f2(ex2(e[2]), ex2(e[3])));
+          }
         }
-      }
+      };
+      // two copies: with the mask as selects every tile would pay for it
+      if (cut) add_tile(std::true_type{});
+      else add_tile(std::false_type{});
       float s0, s1, s2, s3;
       f2_split(acc0, s0, s1);
       f2_split(acc1, s2, s3);
@@ -309,8 +328,6 @@ cudaError_t launch_key_weights(const Tensor4& q, const Tensor4& k, bool f16, int
   // few keys: up to eight CTAs share each tile, until about two per SM exist
   int ranks = 1;
   while (ranks < kMaxCluster && units * ranks * 2 <= 296) ranks *= 2;
-  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), stream);
-  if (e != cudaSuccess) return e;
   return f16 ? launch_typed<true>(p, units, ranks, tq, tk, status, stream)
              : launch_typed<false>(p, units, ranks, tq, tk, status, stream);
 }

@@ -16,12 +16,7 @@ from typing import Optional, Sequence
 import torch
 
 _INT32_MAX = 2**31 - 1
-
-
-def _base():
-    import long_context_hybrid_b200 as base
-    return base
-
+_SCALE = 1.0 / math.sqrt(128)
 
 class Strides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("n", ctypes.c_int64), ("h", ctypes.c_int64)]
@@ -53,78 +48,102 @@ SIGNATURES = {
 }
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 2}
+_bf16, _f16, _f32_t, _i32_t = torch.bfloat16, torch.float16, torch.float32, torch.int32
+_D = 128
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise _base().RtpError(what)
+# These calls are used once per layer and token, so the checks below avoid
+# everything that costs a microsecond on the host: no torch.device objects, no
+# per-call list conversions, no import statements.
+_fns: dict = {}
 
 
-def _same_device(what: str, first: torch.Tensor, *others) -> torch.device:
-    dev = first.device
-    _need(dev.type == "cuda", f"{what}: CUDA tensors only")
-    for t in others:
-        _need(t is None or t.device == dev, f"{what}: tensors on different devices")
+def _fn(name: str):
+    f = _fns.get(name)
+    if f is None:
+        import long_context_hybrid_b200 as base
+        f = _fns[name] = getattr(base.lib(), name)
+    return f
+
+
+def _refuse(what: str):
+    import long_context_hybrid_b200 as base
+    raise base.RtpError(what)
+
+
+def _device(what: str, *tensors) -> int:
+    """Index of the one CUDA device that every tensor (None skipped) is on."""
+    dev = tensors[0].get_device()
+    if dev < 0:
+        _refuse(f"{what}: CUDA tensors only")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse(f"{what}: tensors on different devices")
     return dev
 
 
-def _int32(what: str, t: torch.Tensor, n: Optional[int] = None) -> int:
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and (n is None or t.shape[0] == n),
-          f"{what}: a contiguous int32 vector" + ("" if n is None else f" of {n}"))
+def _int32(what: str, t: torch.Tensor, n: int) -> int:
+    if t.dtype is not _i32_t or t.shape != (n,) or not t.is_contiguous():
+        _refuse(f"{what}: a contiguous int32 vector of {n}")
     return t.data_ptr()
 
 
 def _rows(what: str, t: torch.Tensor, shape, dtype) -> Strides:
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape), f"{what}: expected {dtype} {tuple(shape)}")
-    _need(t.stride(-1) == 1, f"{what}: the last dimension must be contiguous")
-    return Strides(0, t.stride(0), t.stride(1))
+    if t.dtype is not dtype or t.shape != shape:
+        _refuse(f"{what}: expected {dtype} {tuple(shape)}")
+    n, h, d = t.stride()
+    if d != 1:
+        _refuse(f"{what}: the last dimension must be contiguous")
+    return Strides(0, n, h)
 
 
 def _f32(what: str, t: torch.Tensor, shape) -> int:
-    _need(t.dtype == torch.float32 and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{what}: expected contiguous float32 {tuple(shape)}")
+    if t.dtype is not _f32_t or t.shape != shape or not t.is_contiguous():
+        _refuse(f"{what}: expected contiguous float32 {tuple(shape)}")
     return t.data_ptr()
+
+
+def _bounds(cu: torch.Tensor) -> int:
+    if cu.dim() != 1 or cu.shape[0] < 2:
+        _refuse("cu_seqlens: an int32 vector of at least two bounds")
+    return cu.shape[0] - 1
 
 
 @functools.lru_cache(maxsize=256)
 def _head_array(heads: tuple):
-    return (ctypes.c_int32 * len(heads))(*heads)
+    return (ctypes.c_int32 * len(heads))(*[int(h) for h in heads])
 
 
-def _heads(heads: Sequence[int]):
-    h = tuple(int(x) for x in heads)
-    return _head_array(h), len(h)
+def _stream(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _scale(scale: Optional[float], D: int) -> float:
-    return 1.0 / math.sqrt(D) if scale is None else scale
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
+def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
     """Scratch that belongs to the stream it is used on, so that its memory is not handed out before the work ends."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _workspace(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> torch.Tensor:
+def _workspace(nbytes: int, dev: int, ws: Optional[torch.Tensor], stream) -> torch.Tensor:
     if ws is None:
-        return _empty(nbytes, torch.uint8, device, stream)
-    _need(ws.device == device and ws.is_contiguous(), "ws: a contiguous tensor on the call's device")
+        return _empty(nbytes, torch.uint8, dev, stream)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _refuse("ws: a contiguous tensor on the call's device")
     return ws
 
 
-def _run(name: str, dev: torch.device, stream, *args) -> None:
-    """The C call on `stream` (default: the device's current one), with that device current."""
-    base = _base()
-    fn = getattr(base.lib(), name)
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+def _run(name: str, dev: int, *args) -> None:
+    """The C call with its tensors' device current."""
+    if dev == torch._C._cuda_getDevice():
+        status = _fn(name)(*args)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, (stream or torch.cuda.current_stream(dev)).cuda_stream)
-    base._check(status, name)
+            status = _fn(name)(*args)
+    if status != 0:
+        import long_context_hybrid_b200 as base
+        base._check(status, name)
 
 
 class PagedCache:
@@ -138,25 +157,27 @@ class PagedCache:
     ``cache_evict``."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, weights: Optional[torch.Tensor] = None):
-        _need(k.dim() == 4 and k.dtype in _DTYPES and v.shape == k.shape and v.dtype == k.dtype,
-              "PagedCache: k and v [num_pages, page_size, Hkv, D], bf16 or fp16 alike")
-        P, page, Hkv, D = k.shape
-        _need(D == _base().D_HEAD, f"PagedCache: D must be {_base().D_HEAD}")
-        _need(k.stride(3) == 1 and v.stride(3) == 1, "PagedCache: D must be contiguous")
-        _need(table.dim() == 2 and table.dtype == torch.int32 and (table.shape[1] <= 1 or table.stride(1) == 1),
-              "PagedCache: table int32 [B, max_pages] with contiguous rows")
-        self.device = _same_device("PagedCache", k, v, table, weights)
+        shape, dtype = k.shape, k.dtype
+        if len(shape) != 4 or dtype not in _DTYPES or v.shape != shape or v.dtype is not dtype or shape[3] != _D:
+            _refuse(f"PagedCache: k and v [num_pages, page_size, Hkv, {_D}], bf16 or fp16 alike")
+        kp, kn, kh, kd = k.stride()
+        vp, vn, vh, vd = v.stride()
+        if kd != 1 or vd != 1:
+            _refuse("PagedCache: D must be contiguous")
+        if table.dtype is not _i32_t or table.dim() != 2:
+            _refuse("PagedCache: table int32 [B, max_pages]")
+        B, n = table.shape
+        row, step = table.stride()
+        if n > 1 and step != 1:
+            _refuse("PagedCache: the table's rows must be contiguous")
+        self.dev = _device("PagedCache", k, v, table, weights)
+        P, page, Hkv, _ = shape
         w = None if weights is None else _f32("PagedCache: weights", weights, (P, Hkv, page))
         self.k, self.v, self.table, self.weights = k, v, table, weights
-        self.num_pages, self.page_size, self.Hkv, self.D = P, page, Hkv, D
-        B, n = table.shape
-        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), Strides(k.stride(0), k.stride(1), k.stride(2)),
-                                   Strides(v.stride(0), v.stride(1), v.stride(2)), w, table.data_ptr(),
-                                   table.stride(0) if B > 1 else max(n, 1), P, page, n, Hkv)
-
-    @property
-    def capacity(self) -> int:
-        return self.table.shape[1] * self.page_size
+        self.num_pages, self.page_size, self.Hkv, self.D, self.dtype = P, page, Hkv, _D, dtype
+        self.B, self.capacity = B, n * page
+        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), Strides(kp, kn, kh), Strides(vp, vn, vh), w,
+                                   table.data_ptr(), row if B > 1 else max(n, 1), P, page, n, Hkv)
 
 
 def attn_packed(q, k, v, o, heads: Sequence[int], cu_seqlens, window: Optional[int] = None,
@@ -166,18 +187,21 @@ def attn_packed(q, k, v, o, heads: Sequence[int], cu_seqlens, window: Optional[i
     ``cu_seqlens`` int32 [S+1] on the device; writes o[:, heads] (rows of
     sequences) and ``lse`` fp32 [len(heads), T]. ``window`` None: the whole
     prefix."""
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    dev = _same_device("attn_packed", q, k, v, o, cu_seqlens, lse)
-    _need(q.dtype in _DTYPES and D == _base().D_HEAD, "attn_packed: bf16 or fp16, D = 128")
-    qs, ks = _rows("q", q, (T, Hq, D), q.dtype), _rows("k", k, (T, Hkv, D), q.dtype)
-    vs, os_ = _rows("v", v, (T, Hkv, D), q.dtype), _rows("o", o, (T, Hq, D), q.dtype)
-    h, n_heads = _heads(heads)
-    lse_p = None if lse is None else _f32("lse", lse, (n_heads, T))
+    T, Hq, D = shape = q.shape
+    kshape, dtype = k.shape, q.dtype
+    dev = _device("attn_packed", q, k, v, o, cu_seqlens, lse)
+    if dtype not in _DTYPES or D != _D or len(kshape) != 3 or kshape[0] != T or kshape[2] != D:
+        _refuse("attn_packed: q [T, Hq, 128] and k [T, Hkv, 128], bf16 or fp16")
+    S = _bounds(cu_seqlens)
+    heads = _head_array(tuple(heads))
+    n = len(heads)
     buf = _workspace(256, dev, ws, stream)
-    _run("rtp_attn_packed", dev, stream, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), os_,
-         _DTYPES[q.dtype], T, Hq, Hkv, h, n_heads, _int32("cu_seqlens", cu_seqlens), cu_seqlens.shape[0] - 1,
-         _INT32_MAX if window is None else window, _scale(scale, D), lse_p, buf.data_ptr(), buf.nbytes)
+    _run("rtp_attn_packed", dev, q.data_ptr(), _rows("q", q, shape, dtype), k.data_ptr(),
+         _rows("k", k, kshape, dtype), v.data_ptr(), _rows("v", v, kshape, dtype), o.data_ptr(),
+         _rows("o", o, shape, dtype), _DTYPES[dtype], T, Hq, kshape[1], heads, n,
+         _int32("cu_seqlens", cu_seqlens, S + 1), S, _INT32_MAX if window is None else window,
+         _SCALE if scale is None else scale, None if lse is None else _f32("lse", lse, (n, T)), buf.data_ptr(),
+         buf.nbytes, _stream(dev, stream))
     return o
 
 
@@ -188,18 +212,20 @@ def attn_key_weights(q, k, lse, weights, heads: Sequence[int], cu_seqlens, n_obs
     ``n_obs`` rows of its sequence (None: every row), summed over the listed
     heads of its KV head, into ``weights`` fp32 [Hkv, T]; ``lse`` fp32
     [len(heads), T] from ``attn_packed``."""
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    dev = _same_device("attn_key_weights", q, k, lse, weights, cu_seqlens)
-    _need(q.dtype in _DTYPES and D == _base().D_HEAD, "attn_key_weights: bf16 or fp16, D = 128")
-    qs, ks = _rows("q", q, (T, Hq, D), q.dtype), _rows("k", k, (T, Hkv, D), q.dtype)
-    h, n_heads = _heads(heads)
-    lse_p, w_p = _f32("lse", lse, (n_heads, T)), _f32("weights", weights, (Hkv, T))
+    T, Hq, D = shape = q.shape
+    kshape, dtype = k.shape, q.dtype
+    dev = _device("attn_key_weights", q, k, lse, weights, cu_seqlens)
+    if dtype not in _DTYPES or D != _D or len(kshape) != 3 or kshape[0] != T or kshape[2] != D:
+        _refuse("attn_key_weights: q [T, Hq, 128] and k [T, Hkv, 128], bf16 or fp16")
+    S = _bounds(cu_seqlens)
+    heads = _head_array(tuple(heads))
+    n = len(heads)
     buf = _workspace(256, dev, ws, stream)
-    _run("rtp_attn_key_weights", dev, stream, q.data_ptr(), qs, k.data_ptr(), ks, _DTYPES[q.dtype], T, Hq, Hkv, h,
-         n_heads, _int32("cu_seqlens", cu_seqlens), cu_seqlens.shape[0] - 1, lse_p,
-         _INT32_MAX if n_obs is None else n_obs, _INT32_MAX if window is None else window, _scale(scale, D), w_p,
-         buf.data_ptr(), buf.nbytes)
+    _run("rtp_attn_key_weights", dev, q.data_ptr(), _rows("q", q, shape, dtype), k.data_ptr(),
+         _rows("k", k, kshape, dtype), _DTYPES[dtype], T, Hq, kshape[1], heads, n,
+         _int32("cu_seqlens", cu_seqlens, S + 1), S, _f32("lse", lse, (n, T)), _INT32_MAX if n_obs is None else n_obs,
+         _INT32_MAX if window is None else window, _SCALE if scale is None else scale,
+         _f32("weights", weights, (kshape[1], T)), buf.data_ptr(), buf.nbytes, _stream(dev, stream))
     return weights
 
 
@@ -208,16 +234,15 @@ def paged_append(cache: PagedCache, k, v, cu_seqlens, pos, weights: Optional[tor
     ``cu_seqlens`` int32 [S+1]) goes to slot pos[i] + t - cu_seqlens[i] of
     table row i. ``weights`` fp32 [Hkv,T] starts their accumulated weights
     (None: 0)."""
-    T, Hkv, D = k.shape
-    dev = _same_device("paged_append", cache.k, k, v, cu_seqlens, pos, weights)
-    _need(Hkv == cache.Hkv, "paged_append: k has another number of KV heads than the cache")
-    dtype = cache.k.dtype
-    ks, vs = _rows("k", k, (T, Hkv, cache.D), dtype), _rows("v", v, (T, Hkv, cache.D), dtype)
-    S = cu_seqlens.shape[0] - 1
-    _need(S <= cache.table.shape[0], "paged_append: more sequences than table rows")
-    w_p = None if weights is None else _f32("weights", weights, (Hkv, T))
-    _run("rtp_paged_append", dev, stream, cache.struct, k.data_ptr(), ks, v.data_ptr(), vs, w_p, T,
-         _int32("cu_seqlens", cu_seqlens), S, _int32("pos", pos, S))
+    T = k.shape[0]
+    shape, dtype = (T, cache.Hkv, _D), cache.dtype
+    dev = _device("paged_append", cache.k, k, v, cu_seqlens, pos, weights)
+    S = _bounds(cu_seqlens)
+    if S > cache.B:
+        _refuse("paged_append: more sequences than table rows")
+    _run("rtp_paged_append", dev, cache.struct, k.data_ptr(), _rows("k", k, shape, dtype), v.data_ptr(),
+         _rows("v", v, shape, dtype), None if weights is None else _f32("weights", weights, (cache.Hkv, T)), T,
+         _int32("cu_seqlens", cu_seqlens, S + 1), S, _int32("pos", pos, S), _stream(dev, stream))
 
 
 def paged_attn_decode(q, cache: PagedCache, lens, o, heads: Sequence[int], window: Optional[int] = None,
@@ -229,24 +254,27 @@ def paged_attn_decode(q, cache: PagedCache, lens, o, heads: Sequence[int], windo
     ``max_len`` (default: the table's capacity) bounds the lengths. ``lse``
     fp32 [B,len(heads)]; ``weights_out`` (like cache.weights, may be it)
     receives cache.weights plus this token's attention weights."""
-    B, Hq, D = q.shape
-    dev = _same_device("paged_attn_decode", cache.k, q, lens, o, lse, weights_out)
-    dtype = cache.k.dtype
-    qs, os_ = _rows("q", q, (B, Hq, cache.D), dtype), _rows("o", o, (B, Hq, cache.D), dtype)
-    qs, os_ = Strides(qs.n, 0, qs.h), Strides(os_.n, 0, os_.h)
-    _need(B <= cache.table.shape[0], "paged_attn_decode: more sequences than table rows")
-    h, n_heads = _heads(heads)
-    max_len = cache.capacity if max_len is None else max_len
-    window = _INT32_MAX if window is None else window
-    lse_p = None if lse is None else _f32("lse", lse, (B, n_heads))
-    w_p = None
+    B, Hq, _ = q.shape
+    shape, dtype = (B, Hq, _D), cache.dtype
+    dev = _device("paged_attn_decode", cache.k, q, lens, o, lse, weights_out)
+    qs, os_ = _rows("q", q, shape, dtype), _rows("o", o, shape, dtype)
+    qs.b, os_.b = qs.n, os_.n
+    if B > cache.B:
+        _refuse("paged_attn_decode: more sequences than table rows")
+    heads = _head_array(tuple(heads))
+    n = len(heads)
+    if max_len is None:
+        max_len = cache.capacity
+    if window is None:
+        window = _INT32_MAX
+    w = None
     if weights_out is not None:
-        w_p = _f32("weights_out", weights_out, (cache.num_pages, cache.Hkv, cache.page_size))
-    need = _base().lib().rtp_workspace_size_paged_attn_decode(B, max_len, n_heads, window, sink, w_p is not None)
-    buf = _workspace(need, dev, ws, stream)
-    _run("rtp_paged_attn_decode", dev, stream, q.data_ptr(), qs, cache.struct, _int32("lens", lens, B), max_len,
-         o.data_ptr(), os_, _DTYPES[dtype], B, Hq, h, n_heads, window, sink, _scale(scale, D), lse_p, w_p,
-         buf.data_ptr(), buf.nbytes)
+        w = _f32("weights_out", weights_out, (cache.num_pages, cache.Hkv, cache.page_size))
+    buf = _workspace(_fn("rtp_workspace_size_paged_attn_decode")(B, max_len, n, window, sink, w is not None), dev, ws,
+                     stream)
+    _run("rtp_paged_attn_decode", dev, q.data_ptr(), qs, cache.struct, _int32("lens", lens, B), max_len, o.data_ptr(),
+         os_, _DTYPES[dtype], B, Hq, heads, n, window, sink, _SCALE if scale is None else scale,
+         None if lse is None else _f32("lse", lse, (B, n)), w, buf.data_ptr(), buf.nbytes, _stream(dev, stream))
     return o
 
 
@@ -258,21 +286,25 @@ def cache_evict(cache: PagedCache, lens, budget: int, sink: int = 0, recent: int
     weight, moved to slots 0, 1, ... of ``out`` (default: in place). Returns
     (idx int32 [B,Hkv,budget], the kept slots ascending and -1 padded; new_lens
     int32 [B])."""
-    out = cache if out is None else out
+    if out is None:
+        out = cache
     B = lens.shape[0]
-    dev = _same_device("cache_evict", cache.k, lens, out.k, idx, new_lens)
-    _need(cache.k.dtype == out.k.dtype, "cache_evict: caches of different types")
-    _need(cache.weights is not None and out.weights is not None, "cache_evict: both caches need weights")
-    _need(B <= cache.table.shape[0] and B <= out.table.shape[0], "cache_evict: more sequences than table rows")
+    dev = _device("cache_evict", cache.k, lens, out.k, idx, new_lens)
+    if cache.dtype is not out.dtype:
+        _refuse("cache_evict: caches of different types")
+    if cache.weights is None or out.weights is None:
+        _refuse("cache_evict: both caches need weights")
+    if B > cache.B or B > out.B:
+        _refuse("cache_evict: more sequences than table rows")
     if idx is None:
-        idx = _empty((B, cache.Hkv, budget), torch.int32, dev, stream)
+        idx = _empty((B, cache.Hkv, budget), _i32_t, dev, stream)
     if new_lens is None:
-        new_lens = _empty((B,), torch.int32, dev, stream)
-    _need(idx.dtype == torch.int32 and tuple(idx.shape) == (B, cache.Hkv, budget) and idx.is_contiguous(),
-          f"idx: expected contiguous int32 {(B, cache.Hkv, budget)}")
-    max_len = cache.capacity if max_len is None else max_len
-    _run("rtp_cache_evict", dev, stream, cache.struct, out.struct, B, _int32("lens", lens, B), max_len, budget, sink,
-         recent, idx.data_ptr(), _int32("new_lens", new_lens, B))
+        new_lens = _empty((B,), _i32_t, dev, stream)
+    if idx.dtype is not _i32_t or idx.shape != (B, cache.Hkv, budget) or not idx.is_contiguous():
+        _refuse(f"idx: expected contiguous int32 {(B, cache.Hkv, budget)}")
+    _run("rtp_cache_evict", dev, cache.struct, out.struct, B, _int32("lens", lens, B),
+         cache.capacity if max_len is None else max_len, budget, sink, recent, idx.data_ptr(),
+         _int32("new_lens", new_lens, B), _stream(dev, stream))
     return idx, new_lens
 
 
@@ -293,15 +325,15 @@ class PagedLayer:
         self.cache, self.Hq, self.n_obs, self.window, self.sink = cache, Hq, n_obs, window, sink
         self.streaming = list(streaming)
         self.full = [h for h in range(Hq) if h not in set(self.streaming)]
-        _need(not self.streaming or window is not None, "PagedLayer: streaming heads need a window")
-        self.scale = _scale(scale, cache.D)
-        B, dev = cache.table.shape[0], cache.device
-        self.B = B
+        if self.streaming and window is None:
+            _refuse("PagedLayer: streaming heads need a window")
+        self.scale = scale
+        B, dev = cache.B, cache.dev
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
         self.cu_decode = torch.arange(B + 1, dtype=torch.int32, device=dev)
         self.ws_prefill = torch.zeros(256, dtype=torch.uint8, device=dev)
         weighed = cache.weights is not None
-        size = _base().lib().rtp_workspace_size_paged_attn_decode
+        size = _fn("rtp_workspace_size_paged_attn_decode")
         self.ws = torch.empty(max(size(B, cache.capacity, max(1, len(g)), _INT32_MAX if w is None else w, sink, weighed)
                                   for g, w in self._groups()), dtype=torch.uint8, device=dev)
 
@@ -311,7 +343,7 @@ class PagedLayer:
 
     def prefill(self, q, k, v, o, cu_seqlens, stream=None):
         """q/o [T,Hq,D], k/v [T,Hkv,D] of B packed prompts (one per table row)."""
-        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.device)):
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.dev)):
             weights = None
             for heads, window in self._groups():
                 lse = None
@@ -330,7 +362,7 @@ class PagedLayer:
 
     def decode(self, q, k, v, o, stream=None):
         """q/o [B,Hq,D], k/v [B,Hkv,D]: one new token of every sequence."""
-        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.device)):
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.dev)):
             paged_append(self.cache, k, v, self.cu_decode, self.lens)
             self.lens.add_(1)
             for heads, window in self._groups():
@@ -341,7 +373,7 @@ class PagedLayer:
     def evict(self, budget: int, recent: int, stream=None):
         """Shrinks every sequence to ``budget`` tokens per KV head, keeping the
         ``sink`` first and ``recent`` last; returns the kept slots."""
-        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.device)):
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.dev)):
             idx, new_lens = cache_evict(self.cache, self.lens, budget, self.sink, recent)
             self.lens.copy_(new_lens)
         return idx
