@@ -46,13 +46,6 @@ __device__ __forceinline__ int warp_last_le(F f, int n, int64_t t) {
   return lo + __popc(__ballot_sync(0xffffffffu, lane < n && f(lo + lane) <= t)) - 1;
 }
 
-// Sequence of packed row t (cu holds S + 1 non-decreasing entries), or -1
-// when t is in none. The whole warp calls it with one t.
-__device__ __forceinline__ int warp_find_seq(const int32_t* cu, int S, int64_t t) {
-  const int i = warp_last_le([&](int x) -> int64_t { return __ldg(cu + x); }, S + 1, t);
-  return i < S ? i : -1;
-}
-
 // Tiles of `rows` query rows of packed sequences without a list: sequence i
 // owns the tile numbers floor(cu[i] / rows) + i .. floor(cu[i+1] / rows) + i,
 // which are at least ceil(len / rows) of them, so floor(T / rows) + S numbers

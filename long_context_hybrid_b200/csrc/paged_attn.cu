@@ -10,8 +10,10 @@
 //   * The attended slots of a (sequence, KV head) are a segment of 64-key
 //     chunks; the segments of the whole batch form one list that the CTAs (two
 //     per SM) cut into equal runs, so that sequences of any mix of lengths
-//     load every SM alike. The lengths stay on the device: each CTA finds its
-//     run with a scan over them.
+//     load every SM alike. A segment counts kSegCost units more than it has
+//     chunks (in front of them): beginning and ending one costs about as much
+//     as streaming that many. The lengths stay on the device: each CTA finds
+//     its run with a scan over them.
 //   * Each of a CTA's four warps owns 16 keys of every chunk: it resolves
 //     their pages one chunk ahead of the copies, copies the rows with 16-byte
 //     cp.async two chunks ahead into a private three-stage ring (zero-filled
@@ -38,6 +40,8 @@ constexpr int kCtasPerSm = 2;
 constexpr int kChunk = 64;                    // keys per chunk
 constexpr int kKeys = kChunk / kWarps;        // keys per warp and chunk
 constexpr int kStages = 3;
+// 32 sequences of 1 to 16385 tokens (32 / 4 heads): 61 us without it
+constexpr int kSegCost = 3;
 constexpr int kRowBytes = RTP_D * 2;
 constexpr int kSlab = kKeys * kRowBytes;      // one warp's K (or V) rows of one chunk
 constexpr int kGroup = 16;                    // query heads per KV head: rows of the tile
@@ -69,8 +73,7 @@ struct Smem {
   float join[2][kGroup][kPart];
   BlockScanSmem<kThreads> scan;
   unsigned ok[kWarps][kStages];               // which of the 16 keys are there
-  int64_t at_before;
-  int at_b, at_nc;
+  int64_t place[2];                           // a Place
 };
 
 // The attended slots of one sequence: `sink` from the front, then lo .. len-1.
@@ -88,55 +91,91 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
 __device__ __forceinline__ int chunks_of(const DecodeParams& p, int b) {
   return (span_of(p, b).n + kChunk - 1) / kChunk;
 }
+__device__ __forceinline__ int units_of(int chunks) { return chunks > 0 ? chunks + kSegCost : 0; }
 
-// Run c of a list of n chunks cut for n_ctas CTAs (n_ctas <= n).
+// Run c of a list of n units cut for n_ctas CTAs (n_ctas <= n).
 __device__ __forceinline__ int64_t run_start(int c, int64_t n, int n_ctas) { return (int64_t)c * n / n_ctas; }
 __device__ __forceinline__ int cta_of(int64_t x, int64_t n, int n_ctas) {
   return (int)(((x + 1) * n_ctas - 1) / n);
 }
 
-// Chunks of the whole batch (per KV head); every thread of the block calls it.
-__device__ __forceinline__ int64_t total_chunks(const DecodeParams& p, BlockScanSmem<kThreads>& scan) {
-  int64_t all = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    int tot;
-    block_exclusive_scan<kThreads>(b < p.B ? chunks_of(p, b) : 0, tot, scan);
-    all += tot;
-  }
-  return all;
-}
-// Finds the sequence that holds chunk x of the list (x < n_ag * total): its
-// number, its chunks, and the list's chunks before it.
-__device__ __forceinline__ void locate(const DecodeParams& p, int64_t x, BlockScanSmem<kThreads>& scan, int* at_b,
-                                       int* at_nc, int64_t* at_before) {
-  int64_t before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    const int nc = b < p.B ? chunks_of(p, b) : 0;
-    int tot;
-    const int ex = block_exclusive_scan<kThreads>(nc, tot, scan);
-    const int64_t first = (before + ex) * p.n_ag;
-    if (nc > 0 && first <= x && x < first + (int64_t)nc * p.n_ag) {
-      *at_b = b; *at_nc = nc; *at_before = first;
-    }
-    before += tot;
-    if (before * p.n_ag > x) break;
-  }
-  __syncthreads();
-}
+// Where unit x of the list lies: the sequence, its chunks, and the list's
+// units before it.
+struct Place {
+  int64_t before;
+  int b, nc;
+};
 
-// Walks a run: sequence-major, then KV head, then chunk.
+// The scan over the lengths by a block of NT threads: thread i holds sequence
+// i of the batch's last NT sequences (all of it, for most batches). Work
+// says what a sequence holds: chunks(p, b) pieces of work, units(chunks) units.
+template <int NT, class Work>
+struct LenScan {
+  int64_t total;                              // units of the whole batch, per KV head
+  int nc, ex;                                 // this thread's chunks, and the units before it in its block
+  __device__ LenScan(const DecodeParams& p, BlockScanSmem<NT>& scan) {
+    total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
+      const int b = b0 + threadIdx.x;
+      int tot;
+      nc = b < p.B ? Work::chunks(p, b) : 0;
+      ex = block_exclusive_scan<NT>(Work::units(nc), tot, scan);
+      total += tot;
+    }
+  }
+  // Finds the sequence that holds unit x (x < n_ag * total); `at` is shared.
+  __device__ void locate(const DecodeParams& p, int64_t x, BlockScanSmem<NT>& scan, Place* at) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
+      const int b = b0 + threadIdx.x;
+      int tot = 0;
+      if (p.B > NT) {                         // otherwise the first scan still stands
+        nc = b < p.B ? Work::chunks(p, b) : 0;
+        ex = block_exclusive_scan<NT>(Work::units(nc), tot, scan);
+      }
+      const int64_t first = (before + ex) * p.n_ag;
+      if (nc > 0 && first <= x && x < first + (int64_t)Work::units(nc) * p.n_ag) {
+        at->b = b;
+        at->nc = nc;
+        at->before = first;
+      }
+      before += tot;
+      if (before * p.n_ag > x) break;
+    }
+    __syncthreads();
+  }
+};
+
+struct AttendedChunks {
+  static __device__ __forceinline__ int chunks(const DecodeParams& p, int b) { return chunks_of(p, b); }
+  static __device__ __forceinline__ int units(int chunks) { return units_of(chunks); }
+};
+using ChunkScan = LenScan<kThreads, AttendedChunks>;
+
+// Walks the chunks of a run: sequence-major, then KV head, then chunk.
 struct Cursor {
+  int64_t unit;                               // of the current chunk; INT64_MAX past the last
   int b, a, local, nc;
   Span s;
+  __device__ Cursor(const DecodeParams& p, const Place& at, int64_t x) {
+    b = at.b;
+    nc = at.nc;
+    s = span_of(p, b);
+    const int64_t into = x - at.before;
+    a = (int)(into / units_of(nc));
+    const int rem = (int)(into - (int64_t)a * units_of(nc));
+    local = rem > kSegCost ? rem - kSegCost : 0;
+    unit = rem > kSegCost ? x : x + (kSegCost - rem);
+  }
   __device__ void next(const DecodeParams& p) {
+    ++unit;
     if (++local < nc) return;
     local = 0;
+    unit += kSegCost;
     if (++a < p.n_ag) return;
     a = 0;
     do {
-      if (++b >= p.B) { b = p.B - 1; return; }           // past the last run's end
+      if (++b >= p.B) { unit = INT64_MAX; return; }
       nc = chunks_of(p, b);
     } while (nc == 0);
     s = span_of(p, b);
@@ -213,7 +252,8 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
   if (blockIdx.x == 0 && tid == 0) *p.status = 0;
-  const int64_t n_list = total_chunks(p, sm.scan) * p.n_ag;
+  ChunkScan lens(p, sm.scan);
+  const int64_t n_list = lens.total * p.n_ag;
   const int n_ctas = (int)(n_list < gridDim.x ? n_list : gridDim.x);
   // sequences that attend nothing
   for (int x = blockIdx.x * kWarps + warp; x < p.B * p.n_heads; x += gridDim.x * kWarps) {
@@ -221,15 +261,11 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
     if (chunks_of(p, b) == 0) write_row<F16>(p, b, x - b * p.n_heads, 0.f, 0.f, make_float4(0, 0, 0, 0), lane);
   }
   if ((int)blockIdx.x >= n_ctas) return;
-  const int64_t x0 = run_start(blockIdx.x, n_list, n_ctas);
-  const int n_t = (int)(run_start(blockIdx.x + 1, n_list, n_ctas) - x0);
-  locate(p, x0, sm.scan, &sm.at_b, &sm.at_nc, &sm.at_before);
-  Cursor cur;
-  cur.b = sm.at_b;
-  cur.nc = sm.at_nc;
-  cur.a = (int)((x0 - sm.at_before) / cur.nc);
-  cur.local = (int)((x0 - sm.at_before) - (int64_t)cur.a * cur.nc);
-  cur.s = span_of(p, cur.b);
+  const int64_t x0 = run_start(blockIdx.x, n_list, n_ctas), x1 = run_start(blockIdx.x + 1, n_list, n_ctas);
+  Place& place = *reinterpret_cast<Place*>(sm.place);
+  lens.locate(p, x0, sm.scan, &place);
+  Cursor cur(p, place, x0);                   // chunk being computed
+  if (cur.unit >= x1) return;
 
   // this warp's ring and its copies of a chunk into stage st
   const uint32_t ring = su32(sm.ring[warp]);
@@ -242,9 +278,16 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   };
   int slot, page = fetch(slot);
   auto issue = [&](int t) {
-    if (t < n_t) {
+    if (icur.unit < x1) {
       const int st = t % kStages;
       const int g = p.ag_kv[icur.a];
+      if (icur.local == 0 || t == 0) {        // a segment begins: its query rows on their way to L1
+        const int r = lane >> 1;
+        if (r < p.ag_n[icur.a])
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + icur.b * p.q_sb +
+                                                        (int64_t)p.head[p.ag_start[icur.a] + r] * p.q_sh +
+                                                        (lane & 1) * 128));
+      }
       const int64_t r64 = slot < 0 ? 0 : slot & row_mask, pg = page < 0 ? 0 : page;
       const char* krow = p.c.k + pg * p.c.k_sp + r64 * p.c.k_sn + g * p.c.k_sh;
       const char* vrow = p.c.v + pg * p.c.v_sp + r64 * p.c.v_sn + g * p.c.v_sh;
@@ -261,10 +304,8 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
         cp_async16(kdst + slab_off(r, c), ks + c * 16, there);
         cp_async16(vdst + slab_off(r, c), vs + c * 16, there);
       }
-      if (t + 1 < n_t) {
-        icur.next(p);
-        page = fetch(slot);
-      }
+      icur.next(p);
+      if (icur.unit < x1) page = fetch(slot);
     }
     cp_async_commit();                        // one group per chunk, empty past the run
   };
@@ -275,33 +316,35 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   int seg_local = 0;                          // first chunk of this CTA's piece of the segment
   bool first_piece = true, fresh = true;
 
-  // Joins the warps' rows of a finished piece: warps 2, 3 into 0, 1, then 1
-  // into 0, through shared memory; warp 0 ends with the piece's sums in
-  // sm.join[0], and all warps write them out, a row at a time.
-  auto put = [&](float (*to)[kPart]) {
-    if (tq == 0) {
-      to[gq][0] = m_a; to[gq][1] = l_a;
-      to[gq + 8][0] = m_b; to[gq + 8][1] = l_b;
-    }
+  // Joins the warps' rows of a finished piece through shared memory and
+  // writes the piece out, a row at a time. Up to eight rows: the four warps'
+  // partials fit side by side; more: warps 2, 3 go into 0, 1 first.
+  float* const join = &sm.join[0][0][0];
+  auto put = [&](float* to) {                 // rows 0..7, and 8..15 behind them where the group has them
+    if (tq == 0) { to[gq * kPart] = m_a; to[gq * kPart + 1] = l_a; }
 #pragma unroll
-    for (int nt = 0; nt < 16; ++nt) {
-      const int col = 4 + nt * 8 + 2 * tq;
-      *reinterpret_cast<float2*>(&to[gq][col]) = make_float2(o[nt][0], o[nt][1]);
-      *reinterpret_cast<float2*>(&to[gq + 8][col]) = make_float2(o[nt][2], o[nt][3]);
-    }
+    for (int nt = 0; nt < 16; ++nt)
+      *reinterpret_cast<float2*>(to + gq * kPart + 4 + nt * 8 + 2 * tq) = make_float2(o[nt][0], o[nt][1]);
+    if (p.rows <= 8) return;
+    if (tq == 0) { to[(gq + 8) * kPart] = m_b; to[(gq + 8) * kPart + 1] = l_b; }
+#pragma unroll
+    for (int nt = 0; nt < 16; ++nt)
+      *reinterpret_cast<float2*>(to + (gq + 8) * kPart + 4 + nt * 8 + 2 * tq) = make_float2(o[nt][2], o[nt][3]);
   };
-  auto add = [&](const float (*from)[kPart]) {
-    const float xa = from[gq][0], xb = from[gq + 8][0];
+  auto add = [&](const float* from) {
+    const float* fa_ = from + gq * kPart;
+    const float* fb_ = from + (gq + 8) * kPart;
+    const float xa = fa_[0], xb = fb_[0];
     const float na = fmaxf(m_a, xa), nb = fmaxf(m_b, xb);
     const float fa = weight2(m_a, na), fb = weight2(m_b, nb), ga = weight2(xa, na), gb = weight2(xb, nb);
-    l_a = l_a * fa + from[gq][1] * ga;
-    l_b = l_b * fb + from[gq + 8][1] * gb;
+    l_a = l_a * fa + fa_[1] * ga;
+    l_b = l_b * fb + fb_[1] * gb;
     m_a = na; m_b = nb;
 #pragma unroll
     for (int nt = 0; nt < 16; ++nt) {
       const int col = 4 + nt * 8 + 2 * tq;
-      const float2 x = *reinterpret_cast<const float2*>(&from[gq][col]);
-      const float2 y = *reinterpret_cast<const float2*>(&from[gq + 8][col]);
+      const float2 x = *reinterpret_cast<const float2*>(fa_ + col);
+      const float2 y = *reinterpret_cast<const float2*>(fb_ + col);
       o[nt][0] = o[nt][0] * fa + x.x * ga; o[nt][1] = o[nt][1] * fa + x.y * ga;
       o[nt][2] = o[nt][2] * fb + y.x * gb; o[nt][3] = o[nt][3] * fb + y.y * gb;
     }
@@ -311,37 +354,48 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
     l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
     l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
     l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-    if (warp >= 2) put(sm.join[warp - 2]);
-    __syncthreads();
-    if (warp < 2) add(sm.join[warp]);
-    __syncthreads();
-    if (warp == 1) put(sm.join[0]);
-    __syncthreads();
-    if (warp == 0) {
-      add(sm.join[0]);
-      __syncwarp();
-      put(sm.join[0]);
+    int parts, part_rows;
+    if (p.rows <= 8) {
+      parts = kWarps; part_rows = 8;
+      put(join + warp * 8 * kPart);
+    } else {
+      parts = 2; part_rows = kGroup;
+      if (warp >= 2) put(join + (warp - 2) * kGroup * kPart);
+      __syncthreads();
+      if (warp < 2) {
+        add(join + warp * kGroup * kPart);
+        __syncwarp();
+        put(join + warp * kGroup * kPart);
+      }
     }
     __syncthreads();
     const int n = p.ag_n[cur.a], j0 = p.ag_start[cur.a];
     float* part = p.part + ((int64_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * p.rows * kPart;
     for (int r = warp; r < n; r += kWarps) {
-      const float* row = sm.join[0][r];
-      const float4 x = *reinterpret_cast<const float4*>(row + 4 + lane * 4);
+      float m = -INFINITY, l = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < parts; ++w) m = fmaxf(m, join[(w * part_rows + r) * kPart]);
+      for (int w = 0; w < parts; ++w) {
+        const float* from = join + (w * part_rows + r) * kPart;
+        const float f = weight2(from[0], m);
+        const float4 y = *reinterpret_cast<const float4*>(from + 4 + lane * 4);
+        l += f * from[1];
+        x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
+      }
       if (whole) {
-        write_row<F16>(p, cur.b, j0 + r, row[0], row[1], x, lane);
+        write_row<F16>(p, cur.b, j0 + r, m, l, x, lane);
       } else {
         float* to = part + r * kPart;
-        if (lane == 0) { to[0] = row[0]; to[1] = row[1]; }
+        if (lane == 0) { to[0] = m; to[1] = l; }
         *reinterpret_cast<float4*>(to + 4 + lane * 4) = x;
       }
     }
-    __syncthreads();
+    __syncthreads();                          // the buffer is free for the next piece
   };
 
 #pragma unroll
   for (int t = 0; t < kStages - 1; ++t) issue(t);
-  for (int t = 0; t < n_t; ++t) {
+  for (int t = 0; cur.unit < x1; ++t, cur.next(p)) {
     issue(t + kStages - 1);
     if (fresh) {
       fresh = false;
@@ -453,12 +507,11 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
     }
     __syncwarp();                             // stage st is free for chunk t + kStages
     const bool seg_end = cur.local + 1 == cur.nc;
-    if (seg_end || t + 1 == n_t) {
+    if (seg_end || cur.unit + 1 == x1) {
       finish(seg_end && seg_local == 0);
       first_piece = false;
       fresh = true;
     }
-    if (t + 1 < n_t) cur.next(p);
   }
   cp_async_wait<0>();
 }
@@ -470,29 +523,33 @@ template <bool F16>
 __global__ void __launch_bounds__(kThreads)
 paged_join_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ BlockScanSmem<kThreads> scan;
-  __shared__ int at_b, at_nc;
-  __shared__ int64_t at_before;
+  __shared__ Place place;
   __shared__ float wm[kWarps], wl[kWarps];
   __shared__ float4 wo[kWarps][32];
-  pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t n_list = total_chunks(p, scan) * p.n_ag;
+  // which pieces to join depends on the lengths alone, which were complete
+  // before the first kernel let this one start; the pieces are awaited below
+  ChunkScan lens(p, scan);
+  const int64_t n_list = lens.total * p.n_ag;
   const int n_ctas = (int)(n_list < gridDim.x ? n_list : gridDim.x);
-  const int c = blockIdx.x;
-  if (c == 0 || c >= n_ctas) return;
-  const int64_t x = run_start(c, n_list, n_ctas);
-  locate(p, x, scan, &at_b, &at_nc, &at_before);
-  const int b = at_b, nc = at_nc;
-  const int a = (int)((x - at_before) / nc);
-  const int64_t s0 = at_before + (int64_t)a * nc;         // the segment is [s0, s0 + nc)
-  if (x == s0 || run_start(c - 1, n_list, n_ctas) > s0) return;
-  const int r = blockIdx.y;
-  if (r >= p.ag_n[a]) return;
-  const int c_last = cta_of(s0 + nc - 1, n_list, n_ctas);
-  // piece i comes from run c - 1 + i; the first is that run's last piece
-  // unless the run starts with the segment
-  const int n = c_last - (c - 1) + 1;
-  const int slot0 = (c - 1) * 2 + (run_start(c - 1, n_list, n_ctas) == s0 ? 0 : 1);
+  const int c = blockIdx.x, r = blockIdx.y;
+  int b = 0, a = 0, n = 0, slot0 = 0;          // sequence, listed KV head, pieces, first piece
+  if (c > 0 && c < n_ctas) {
+    const int64_t x = run_start(c, n_list, n_ctas);
+    lens.locate(p, x, scan, &place);
+    b = place.b;
+    const int units = units_of(place.nc);
+    a = (int)((x - place.before) / units);
+    const int64_t u0 = place.before + (int64_t)a * units, s0 = u0 + kSegCost;   // chunks at [s0, s0 + nc)
+    const int64_t x_prev = run_start(c - 1, n_list, n_ctas);
+    // piece i comes from run c - 1 + i; the first is that run's last piece
+    // unless nothing lies before the segment in it
+    if (x > s0 && x_prev <= s0 && r < p.ag_n[a]) n = cta_of(s0 + place.nc - 1, n_list, n_ctas) - (c - 1) + 1;
+    slot0 = (c - 1) * 2 + (x_prev >= u0 ? 0 : 1);
+  }
+  pdl_wait();                                 // every block: the next kernel relies on it
+  if (n == 0) return;
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kBatch = 8;
@@ -541,32 +598,73 @@ paged_join_kernel(const __grid_constant__ DecodeParams p) {
 }
 
 // w_out = w + sum over the group's listed heads of exp(score - lse), for
-// every slot of the sequence that is in a page.
+// every slot of the sequence that is in a page. Bound by L2 and HBM: 8 bytes
+// of weights and 4 bytes of score per listed head a slot. The batch's blocks of
+// 256 slots form a list cut into equal runs, as above.
 namespace {
 constexpr int kWeightThreads = 256;
-}
+constexpr int kWeightCtas = 148 * 8;
+struct SlotBlocks {
+  static __device__ __forceinline__ int chunks(const DecodeParams& p, int b) {
+    return (int)(((int64_t)seq_len(p.lens, b, p.max_len) + kWeightThreads - 1) / kWeightThreads);
+  }
+  static __device__ __forceinline__ int units(int chunks) { return chunks; }
+};
+}  // namespace
 __global__ void __launch_bounds__(kWeightThreads)
 paged_weights_kernel(const __grid_constant__ DecodeParams p) {
-  pdl_wait();
-  const int b = blockIdx.z, a = blockIdx.y;
-  const Span s = span_of(p, b);
-  const int u = blockIdx.x * kWeightThreads + threadIdx.x;
-  if (u >= s.len) return;
-  const int page = page_of(p.c, b, u);
-  if (page < 0) return;
-  const int g = p.ag_kv[a], n = p.ag_n[a], j0 = p.ag_start[a];
-  float sum = 0.f;
-  const int e = u < s.sink ? u : (u >= s.lo ? u - s.lo + s.sink : -1);
-  if (e >= 0) {
-    const float* at = p.logits + ((int64_t)b * p.n_heads + j0) * p.att_cap + e;
-    const float* lse2 = p.lse2 + (int64_t)b * p.n_heads + j0;
-    for (int r = 0; r < n; ++r) {
-      const float l2 = lse2[r];
-      sum += l2 == -INFINITY ? 0.f : exp2f(at[r * p.att_cap] - l2);
+  __shared__ BlockScanSmem<kWeightThreads> scan;
+  __shared__ Place place;
+  // Lengths, tables and the old weights are complete before this call's first
+  // kernel lets the next one start; only scores and lse come from this call.
+  LenScan<kWeightThreads, SlotBlocks> lens(p, scan);
+  const int64_t n_list = lens.total * p.n_ag;
+  const int n_ctas = (int)(n_list < gridDim.x ? n_list : gridDim.x);
+  if ((int)blockIdx.x >= n_ctas) {
+    pdl_wait();
+    return;
+  }
+  const int64_t x0 = run_start(blockIdx.x, n_list, n_ctas), x1 = run_start(blockIdx.x + 1, n_list, n_ctas);
+  lens.locate(p, x0, scan, &place);
+  int b = place.b, nc = place.nc, a = (int)((x0 - place.before) / nc);
+  int block = (int)((x0 - place.before) - (int64_t)a * nc);
+  for (int64_t x = x0; x < x1; ++x) {
+    const Span s = span_of(p, b);
+    const int u = block * kWeightThreads + threadIdx.x;
+    const int page = u < s.len ? page_of(p.c, b, u) : -1;
+    if (page >= 0) {
+      const int g = p.ag_kv[a], n = p.ag_n[a], j0 = p.ag_start[a];
+      const int64_t w = (((int64_t)page * p.c.Hkv + g) << p.c.page_shift) + (u & ((1 << p.c.page_shift) - 1));
+      const float before = p.c.w[w];
+      if (x == x0) pdl_wait();
+      float sum = 0.f;
+      const int e = u < s.sink ? u : (u >= s.lo ? u - s.lo + s.sink : -1);
+      if (e >= 0) {
+        const float* at = p.logits + ((int64_t)b * p.n_heads + j0) * p.att_cap + e;
+        const float* lse2 = p.lse2 + (int64_t)b * p.n_heads + j0;
+        constexpr int kAhead = 8;             // scores a thread keeps in flight
+        for (int r0 = 0; r0 < n; r0 += kAhead) {
+          float x_[kAhead], l_[kAhead];
+#pragma unroll
+          for (int r = 0; r < kAhead; ++r) {
+            x_[r] = r0 + r < n ? at[(r0 + r) * p.att_cap] : -INFINITY;
+            l_[r] = r0 + r < n ? lse2[r0 + r] : 0.f;
+          }
+#pragma unroll
+          for (int r = 0; r < kAhead; ++r) sum += l_[r] == -INFINITY ? 0.f : exp2f(x_[r] - l_[r]);
+        }
+      }
+      p.w_out[w] = before + sum;
+    }
+    if (x == x0) pdl_wait();                  // the threads without a slot in the first block, too
+    if (++block == nc && x + 1 < x1) {
+      block = 0;
+      if (++a == p.n_ag) {
+        a = 0;
+        do nc = SlotBlocks::chunks(p, ++b); while (nc == 0);
+      }
     }
   }
-  const int64_t w = (((int64_t)page * p.c.Hkv + g) << p.c.page_shift) + (u & ((1 << p.c.page_shift) - 1));
-  p.w_out[w] = p.c.w[w] + sum;
 }
 
 namespace {
@@ -652,8 +750,9 @@ cudaError_t launch_paged_decode(const PagedView& c, const void* q, int64_t q_sb,
   e = f16 ? launch_typed<true>(p, (int)grid, stream) : launch_typed<false>(p, (int)grid, stream);
   if (e != cudaSuccess) return e;
   if (w_out) {
-    const dim3 g((max_len + kWeightThreads - 1) / kWeightThreads, p.n_ag, B);
-    e = launch_pdl(paged_weights_kernel, g, dim3(kWeightThreads), 0, stream, p);
+    const int64_t blocks = ((int64_t)max_len + kWeightThreads - 1) / kWeightThreads * p.n_ag * B;
+    e = launch_pdl(paged_weights_kernel, dim3((unsigned)(blocks < kWeightCtas ? blocks : kWeightCtas)),
+                   dim3(kWeightThreads), 0, stream, p);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();

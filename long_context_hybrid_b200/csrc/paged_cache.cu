@@ -1,9 +1,9 @@
 // The paged cache: filling it and shrinking it.
 //
 // rtp_paged_append copies packed K/V rows (and weights) to their slots; it
-// moves 1 KB per token and KV head and is bound by HBM. A CTA takes a few
-// consecutive tokens: one warp per token finds its sequence, page and row,
-// then all threads copy 16-byte pieces.
+// moves 1 KB per token and KV head and is bound by HBM. A CTA takes up to 32
+// consecutive tokens: one warp finds their sequences, pages and rows (a lane
+// each), then the warps copy whole rows in 16-byte pieces.
 //
 // rtp_cache_evict keeps, per KV head, the first `sink` tokens, the last
 // `recent` and the budget - sink - recent others of largest accumulated
@@ -11,10 +11,12 @@
 //   * selection, one thread-block cluster per (sequence, KV head): every CTA
 //     holds the order-preserving keys of a contiguous slice of the candidates
 //     in shared memory (read once through the page table); the threshold key is
-//     found by three radix passes (11, 11, 10 bits) whose histograms are summed
-//     over distributed shared memory; the CTAs then exchange their counts and
-//     write their slice of the ascending list. Nothing depends on the order of
-//     atomics: counts are integers and ties go to the lower slot;
+//     found by four radix passes of 8 bits whose histograms are summed over
+//     distributed shared memory; the CTAs then exchange their counts and write
+//     their slice of the ascending list. Nothing depends on the order of
+//     atomics: counts are integers and ties go to the lower slot. (Passes of 11
+//     bits are fewer, but every CTA then reads 64 KB of its neighbours'
+//     histograms a pass: 22 against 16 us for 8 x 4 rows of 5000 to 32768);
 //   * the move, bound by HBM: 512 bytes of K and V read and written per kept
 //     token and KV head.
 #include <cooperative_groups.h>
@@ -30,7 +32,8 @@ namespace {
 // Append
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 8;               // most tokens of one CTA: one per warp
+constexpr int kAppendTokens = 32;              // most tokens of one CTA: one per lane
+constexpr int kAppendAhead = 8;                // rows a warp keeps in flight
 
 struct AppendParams {
   PagedView c;
@@ -47,37 +50,50 @@ paged_append_kernel(const AppendParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * p.per_cta;
   const int n = min(p.per_cta, p.T - t0);
-  if (warp < n) {
-    const int t = t0 + warp;
-    const int i = warp_find_seq(p.cu, p.S, t);
-    if (lane == 0) {
-      int page = -1, row = 0;
-      if (i >= 0) {
-        const int64_t slot = (int64_t)__ldg(p.pos + i) + t - __ldg(p.cu + i);
-        if (slot >= 0 && slot < p.c.capacity) {
-          page = page_of(p.c, i, slot);
-          row = (int)(slot & ((1 << p.c.page_shift) - 1));
-        }
+  if (warp == 0) {
+    // the sequence of the first token, then every lane goes on to its own
+    int i = max(0, warp_last_le([&](int x) -> int64_t { return __ldg(p.cu + x); }, p.S + 1, t0));
+    const int t = t0 + lane;
+    while (i < p.S && __ldg(p.cu + i + 1) <= t) ++i;
+    int page = -1, row = 0;
+    if (lane < n && i < p.S && __ldg(p.cu + i) <= t) {
+      const int64_t slot = (int64_t)__ldg(p.pos + i) + t - __ldg(p.cu + i);
+      if (slot >= 0 && slot < p.c.capacity) {
+        page = page_of(p.c, i, slot);
+        row = (int)(slot & ((1 << p.c.page_shift) - 1));
       }
-      s_page[warp] = page;
-      s_row[warp] = row;
     }
+    s_page[lane] = page;
+    s_row[lane] = row;
   }
   __syncthreads();
-  const int per_token = p.c.Hkv * 32;          // 16-byte pieces of a token's K and V rows
-  for (int x = threadIdx.x; x < n * per_token; x += kAppendThreads) {
-    const int j = x / per_token, y = x - j * per_token;
-    const int page = s_page[j];
-    if (page < 0) continue;
-    const int h = y >> 5, c = y & 31;          // lanes 0..15: the K row, 16..31: the V row
-    const int64_t t = t0 + j, row = s_row[j];
-    if (c < 16) {
-      const uint4 d = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_sn + h * p.k_sh) + c);
-      *(reinterpret_cast<uint4*>(p.c.k + page * p.c.k_sp + row * p.c.k_sn + h * p.c.k_sh) + c) = d;
-    } else {
-      const uint4 d = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_sn + h * p.v_sh) + (c - 16));
-      *(reinterpret_cast<uint4*>(p.c.v + page * p.c.v_sp + row * p.c.v_sn + h * p.c.v_sh) + (c - 16)) = d;
+  // a warp moves whole rows: lanes 0..15 the K row, 16..31 the V row of one
+  // token and head; kAppendAhead rows' loads are in flight at once
+  const int c = (lane & 15) * 16;
+  const char* from = lane < 16 ? p.k + c : p.v + c;
+  const int64_t from_n = lane < 16 ? p.k_sn : p.v_sn, from_h = lane < 16 ? p.k_sh : p.v_sh;
+  char* to = lane < 16 ? p.c.k + c : p.c.v + c;
+  const int64_t to_p = lane < 16 ? p.c.k_sp : p.c.v_sp, to_n = lane < 16 ? p.c.k_sn : p.c.v_sn,
+                to_h = lane < 16 ? p.c.k_sh : p.c.v_sh;
+  const int rows = n * p.c.Hkv;
+  for (int x0 = warp; x0 < rows; x0 += kAppendAhead * (kAppendThreads / 32)) {
+    uint4 d[kAppendAhead];
+    char* at[kAppendAhead];
+#pragma unroll
+    for (int y = 0; y < kAppendAhead; ++y) {
+      const int x = x0 + y * (kAppendThreads / 32);
+      at[y] = nullptr;
+      if (x < rows) {
+        const int j = x / p.c.Hkv, h = x - j * p.c.Hkv;
+        if (s_page[j] >= 0) {
+          at[y] = to + s_page[j] * to_p + s_row[j] * to_n + h * to_h;
+          d[y] = __ldg(reinterpret_cast<const uint4*>(from + (int64_t)(t0 + j) * from_n + h * from_h));
+        }
+      }
     }
+#pragma unroll
+    for (int y = 0; y < kAppendAhead; ++y)
+      if (at[y]) *reinterpret_cast<uint4*>(at[y]) = d[y];
   }
   if (p.c.w) {
     for (int x = threadIdx.x; x < n * p.c.Hkv; x += kAppendThreads) {
@@ -96,7 +112,8 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxCluster = 8;
 constexpr int kSelKeys = 40960;                // keys a CTA keeps in shared memory (160 KB)
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
+constexpr int kCopies = 8;                     // of a CTA's histogram: weights share few exponents
 
 struct EvictParams {
   PagedView src, dst;
@@ -107,18 +124,60 @@ struct EvictParams {
 };
 
 struct SelectSmem {
-  uint32_t hist[kBins];                        // this CTA's counts, read by its cluster
-  uint32_t sum[kBins];                         // the cluster's
-  BlockScanSmem<kSelThreads> scan;
-  int above, equal;                            // this CTA's keys above / at the threshold
+  uint32_t copies[kCopies][kBins];             // lane l counts in copy l % kCopies
+  uint32_t hist[2][kBins];                     // their sums (passes alternate), read by the cluster
+  int warp_sum[kBins / 32];
+  int above, equal;                            // this CTA's keys above / at the threshold, read by its cluster
   int digit, before;
   int warp_above[kSelWarps], warp_equal[kSelWarps];
 };
 
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ int warp_scan(int x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Sums the cluster's histograms (thread t < 256: bin 255 - t, so that sums run
+// from the top bin down) and finds the digit that holds the `left`-th key.
+// Every rank's count is loaded at once: a round trip to another CTA's shared
+// memory takes as long as one to L2. The whole block calls it.
+__device__ __forceinline__ void find_digit(cg::cluster_group& cluster, SelectSmem& sm, const uint32_t* hist,
+                                           int n_ranks, int left) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bin = kBins - 1 - tid;
+  int count = 0, incl = 0;
+  if (tid < kBins) {
+    uint32_t c[kSelMaxCluster];                          // past the last rank, its again
+#pragma unroll
+    for (int r = 0; r < kSelMaxCluster; ++r)
+      c[r] = cluster.map_shared_rank(const_cast<uint32_t*>(hist), min(r, n_ranks - 1))[bin];
+#pragma unroll
+    for (int r = 0; r < kSelMaxCluster; ++r) count += r < n_ranks ? (int)c[r] : 0;
+    incl = warp_scan(count);
+    if (lane == 31) sm.warp_sum[warp] = incl;
+  }
+  __syncthreads();
+  if (tid < kBins) {
+    int before = lane < warp ? sm.warp_sum[lane] : 0;    // warp < 8
+    before = __reduce_add_sync(0xffffffffu, before) + incl - count;
+    if (before < left && before + count >= left) {
+      sm.digit = bin;
+      sm.before = before;
+    }
+  }
+  __syncthreads();
+}
+
 // Order-preserving key of a weight; NaN ranks above every number.
 __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xffffffffu : f2key(w); }
 
-__global__ void __launch_bounds__(kSelThreads, 1)
+__global__ void __launch_bounds__(kSelThreads, 2)
 evict_select_kernel(const EvictParams p, int n_keys) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_raw);
@@ -149,68 +208,83 @@ evict_select_kernel(const EvictParams p, int n_keys) {
   const int per = (n_cand + n_ranks - 1) / n_ranks;
   const int c0 = min(n_cand, rank * per), n = min(n_cand, c0 + per) - c0;
   const int first = p.sink + c0;               // slot of the slice's key 0
-  auto load_key = [&](int i) -> uint32_t {
-    const int slot = first + i;
-    const int page = page_of(p.src, b, slot);
-    if (page < 0) return 0u;                   // a token that is not there ranks last
-    return weight_key(p.src.w[(((int64_t)page * p.src.Hkv + g) << p.src.page_shift) +
-                              (slot & ((1 << p.src.page_shift) - 1))]);
+  // keys i, i + step, .. below end of the slice, from the pages. Every load is
+  // unconditional (clamped to the last key, or to page 0) and none is used
+  // before all of its kind are under way: under a condition the compiler
+  // waits for them one by one (measured: 6 us for eight instead of 2).
+  constexpr int kAhead = 8;
+  const int row_mask = (1 << p.src.page_shift) - 1;
+  const int32_t* table = p.src.table + (int64_t)b * p.src.table_stride;
+  auto load_keys = [&](int i, int step_, int end, uint32_t (&x)[kAhead]) {
+    int page[kAhead];
+    float w[kAhead];
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) page[y] = __ldg(table + ((first + min(i + y * step_, end - 1)) >> p.src.page_shift));
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const int64_t from = (unsigned)page[y] < (unsigned)p.src.num_pages ? page[y] : 0;
+      w[y] = p.src.w[((from * p.src.Hkv + g) << p.src.page_shift) + ((first + min(i + y * step_, end - 1)) & row_mask)];
+    }
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y)           // a token that is not there ranks last
+      x[y] = (unsigned)page[y] < (unsigned)p.src.num_pages ? weight_key(w[y]) : 0u;
   };
   const int n_smem = min(n, n_keys);
-  constexpr int kAhead = 8;                    // loads a thread keeps in flight
-  for (int i0 = tid; i0 < n_smem; i0 += kAhead * kSelThreads) {
+  for (int i = tid; i < n_smem; i += kAhead * kSelThreads) {
     uint32_t x[kAhead];
+    load_keys(i, kSelThreads, n_smem, x);
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + a * kSelThreads;
-      x[a] = i < n_smem ? load_key(i) : 0u;
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + a * kSelThreads;
-      if (i < n_smem) keys[i] = x[a];
-    }
+    for (int y = 0; y < kAhead; ++y)
+      if (i + y * kSelThreads < n_smem) keys[i + y * kSelThreads] = x[y];
   }
-  auto key = [&](int i) -> uint32_t { return i < n_smem ? keys[i] : load_key(i); };
+  // f(i, key) for i = from, from + stride, .. below end: from shared memory, and
+  // what did not fit there from the pages again
+  auto each_key = [&](int from, int stride, int end, auto f) {
+    const int near = min(end, n_smem);
+    int i = from;
+    for (; i < near; i += kAhead * stride) {
+      uint32_t x[kAhead];
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y) x[y] = keys[min(i + y * stride, near - 1)];
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y)
+        if (i + y * stride < near) f(i + y * stride, x[y]);
+    }
+    if (end > n_smem) {
+      i = from + (max(0, n_smem - from) + stride - 1) / stride * stride;
+      for (; i < end; i += kAhead * stride) {
+        uint32_t x[kAhead];
+        load_keys(i, stride, end, x);
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y)
+          if (i + y * stride < end) f(i + y * stride, x[y]);
+      }
+    }
+  };
 
   uint32_t prefix = 0, mask = 0;
   int left = need;                             // still to take among the keys matching the prefix
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const int bins = pass == 2 ? 1024 : 2048;
-    for (int x = tid; x < bins; x += kSelThreads) sm.hist[x] = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    uint32_t* hist = sm.hist[(shift >> 3) & 1];          // the other one may still be read by the cluster
+    for (int x = tid; x < kCopies * kBins; x += kSelThreads) (&sm.copies[0][0])[x] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t x = key(i);
-      if ((x & mask) == prefix) atomicAdd(&sm.hist[(x >> shift) & (bins - 1)], 1u);
+    uint32_t* mine = sm.copies[lane % kCopies];
+    each_key(tid, kSelThreads, n, [&](int, uint32_t x) {
+      if ((x & mask) == prefix) atomicAdd(&mine[(x >> shift) & (kBins - 1)], 1u);
+    });
+    __syncthreads();
+    if (tid < kBins) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int y = 0; y < kCopies; ++y) c += sm.copies[y][tid];
+      hist[tid] = c;
     }
     cluster.sync();
-    // thread t owns the bins bins - 1 - t * per_t ... walking downwards
-    const int per_t = bins / kSelThreads;
-    int local = 0;
-    for (int q = 0; q < per_t; ++q) {
-      const int x = bins - 1 - (tid * per_t + q);
-      uint32_t s = 0;
-      for (int r = 0; r < n_ranks; ++r) s += cluster.map_shared_rank(sm.hist, r)[x];
-      sm.sum[x] = s;
-      local += (int)s;
-    }
-    int total;
-    const int before = block_exclusive_scan<kSelThreads>(local, total, sm.scan);
-    if (before < left && before + local >= left) {
-      int run = before;
-      for (int q = 0; q < per_t; ++q) {
-        const int x = bins - 1 - (tid * per_t + q);
-        const int s = (int)sm.sum[x];
-        if (run + s >= left) { sm.digit = x; sm.before = run; break; }
-        run += s;
-      }
-    }
-    cluster.sync();                            // the digit is set, and every CTA has read the histograms
+    find_digit(cluster, sm, hist, n_ranks, left);
     left -= sm.before;
     prefix |= (uint32_t)sm.digit << shift;
-    mask |= (uint32_t)(bins - 1) << shift;
+    mask |= 255u << shift;
   }
   // every key above `prefix` is taken, and the `left` lowest slots equal to it
 
@@ -218,41 +292,49 @@ evict_select_kernel(const EvictParams p, int n_keys) {
   const int per_w = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
   const int w0 = min(n, warp * per_w), w1 = min(n, w0 + per_w);
   int above = 0, equal = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t x = key(i);
+  each_key(w0 + lane, 32, w1, [&](int, uint32_t x) {
     above += x > prefix;
     equal += x == prefix;
-  }
+  });
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);
   if (lane == 0) { sm.warp_above[warp] = above; sm.warp_equal[warp] = equal; }
   __syncthreads();
-  if (tid == 0) {
-    int a = 0, e = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      const int xa = sm.warp_above[w], xe = sm.warp_equal[w];
-      sm.warp_above[w] = a; sm.warp_equal[w] = e;
-      a += xa; e += xe;
-    }
-    sm.above = a; sm.equal = e;
+  const int wa = lane < kSelWarps ? sm.warp_above[lane] : 0, we = lane < kSelWarps ? sm.warp_equal[lane] : 0;
+  if (warp == 0) {
+    const int a = __reduce_add_sync(0xffffffffu, wa), e = __reduce_add_sync(0xffffffffu, we);
+    if (lane == 0) { sm.above = a; sm.equal = e; }
   }
   cluster.sync();
-  int a0 = sm.warp_above[warp], e0 = sm.warp_equal[warp];   // before this warp's part, over the cluster
-  for (int r = 0; r < rank; ++r) {
-    a0 += *cluster.map_shared_rank(&sm.above, r);
-    e0 += *cluster.map_shared_rank(&sm.equal, r);
+  // taken before this warp's part, over the cluster: lane r looks at rank r and warp r
+  int a0 = lane < warp ? wa : 0, e0 = lane < warp ? we : 0;
+  if (lane < rank) {
+    a0 += *cluster.map_shared_rank(&sm.above, lane);
+    e0 += *cluster.map_shared_rank(&sm.equal, lane);
   }
-  for (int i0 = w0; i0 < w1; i0 += 32) {
+  a0 = __reduce_add_sync(0xffffffffu, a0);
+  e0 = __reduce_add_sync(0xffffffffu, e0);
+  const unsigned below = (1u << lane) - 1u;
+  for (int i0 = w0; i0 < w1; i0 += kAhead * 32) {
+    uint32_t x[kAhead];
     const int i = i0 + lane;
-    const uint32_t x = i < w1 ? key(i) : 0u;
-    const unsigned ab = __ballot_sync(0xffffffffu, i < w1 && x > prefix);
-    const unsigned eq = __ballot_sync(0xffffffffu, i < w1 && x == prefix);
-    const unsigned below = (1u << lane) - 1u;
-    const int ea = e0 + __popc(eq & below);
-    const bool take = ((ab >> lane) & 1u) || (((eq >> lane) & 1u) && ea < left);
-    if (take) out[p.sink + a0 + __popc(ab & below) + min(ea, left)] = first + i;
-    a0 += __popc(ab);
-    e0 += __popc(eq);
+    if (min(w1, i0 + kAhead * 32) <= n_smem) {
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y) x[y] = keys[min(i + y * 32, w1 - 1)];
+    } else {
+      load_keys(i, 32, w1, x);
+    }
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const bool in = i + y * 32 < w1;
+      const unsigned ab = __ballot_sync(0xffffffffu, in && x[y] > prefix);
+      const unsigned eq = __ballot_sync(0xffffffffu, in && x[y] == prefix);
+      const int ea = e0 + __popc(eq & below);
+      const bool take = ((ab >> lane) & 1u) || (((eq >> lane) & 1u) && ea < left);
+      if (take) out[p.sink + a0 + __popc(ab & below) + min(ea, left)] = first + i + y * 32;
+      a0 += __popc(ab);
+      e0 += __popc(eq);
+    }
   }
   cluster.sync();                              // no CTA leaves while its counts may be read
 }
@@ -393,8 +475,9 @@ cudaError_t launch_paged_append(const PagedView& c, const void* k, int64_t k_sn,
   p.v = static_cast<const char*>(v); p.v_sn = v_sn * 2; p.v_sh = v_sh * 2;
   p.w = w; p.w_sh = T;
   p.cu = cu; p.pos = pos; p.S = S; p.T = T;
-  // few tokens: one per CTA, so that they spread over the SMs
-  p.per_cta = T >= 8 * 148 ? kAppendTokens : 1;
+  // few tokens spread over the SMs; many share a CTA and its search (8 a CTA: 25 us
+  // for 26477 tokens of 4 heads)
+  p.per_cta = T / 148 < 1 ? 1 : (T / 148 < kAppendTokens ? T / 148 : kAppendTokens);
   paged_append_kernel<<<(T + p.per_cta - 1) / p.per_cta, kAppendThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
