@@ -1,22 +1,22 @@
 """Serving calls: packed prompts, a paged key-value cache and its eviction.
 
-Marshalling for the serving part of ``include/rtp.h`` and ``PagedLayer``,
-which runs the calls of one layer in order. Arguments that the C side cannot
-see (dtypes, shapes, devices, contiguity) are checked here and raise
-``RtpError``; the rest is checked by the C calls. Work goes to the current
-stream of the tensors' device.
+The serving part of ``include/rtp.h`` on torch tensors, and ``PagedLayer``,
+which runs the calls of one layer in order. The native module ``_marshal``
+reads the tensors; what the C side cannot see (dtypes, shapes, devices,
+contiguity) it checks and refuses with ``RtpError``, the rest is checked by the
+C calls. Work goes to the given stream, or the current one of the tensors'
+device.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
-import math
+import struct
 from typing import Optional, Sequence
 
 import torch
 
 _INT32_MAX = 2**31 - 1
-_SCALE = 1.0 / math.sqrt(128)
 
 class Strides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("n", ctypes.c_int64), ("h", ctypes.c_int64)]
@@ -47,103 +47,59 @@ SIGNATURES = {
     "rtp_cache_evict": (_I, [_C, _C, _I, _P, _I, _I, _I, _I, _P, _P, _P]),
 }
 
-_DTYPES = {torch.bfloat16: 0, torch.float16: 2}
-_bf16, _f16, _f32_t, _i32_t = torch.bfloat16, torch.float16, torch.float32, torch.int32
-_D = 128
+_native = None
 
 
-# These calls are used once per layer and token, so the checks below avoid
-# everything that costs a microsecond on the host: no torch.device objects, no
-# per-call list conversions, no import statements.
-_fns: dict = {}
-
-
-def _fn(name: str):
-    f = _fns.get(name)
-    if f is None:
+def _marshal():
+    """The ``_marshal`` module, set up with the library's functions (raises if either has not been built)."""
+    global _native
+    if _native is None:
         import long_context_hybrid_b200 as base
-        f = _fns[name] = getattr(base.lib(), name)
-    return f
+        lib = base.lib()
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise base.RtpError("_marshal.so is missing: build it with "
+                                "`python -m long_context_hybrid_b200.build`") from e
+
+        def address(name):
+            return ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+
+        module.setup(base.RtpError, base._check, torch.bfloat16, torch.float16, torch.float32, torch.int32,
+                     torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, address("rtp_attn_packed"),
+                     address("rtp_attn_key_weights"), address("rtp_paged_append"), address("rtp_paged_attn_decode"),
+                     address("rtp_cache_evict"), address("rtp_workspace_size_paged_attn_decode"))
+        _native = module
+    return _native
 
 
-def _refuse(what: str):
-    import long_context_hybrid_b200 as base
-    raise base.RtpError(what)
-
-
-def _device(what: str, *tensors) -> int:
-    """Index of the one CUDA device that every tensor (None skipped) is on."""
-    dev = tensors[0].get_device()
-    if dev < 0:
-        _refuse(f"{what}: CUDA tensors only")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            _refuse(f"{what}: tensors on different devices")
-    return dev
-
-
-def _int32(what: str, t: torch.Tensor, n: int) -> int:
-    if t.dtype is not _i32_t or t.shape != (n,) or not t.is_contiguous():
-        _refuse(f"{what}: a contiguous int32 vector of {n}")
-    return t.data_ptr()
-
-
-def _rows(what: str, t: torch.Tensor, shape, dtype) -> Strides:
-    if t.dtype is not dtype or t.shape != shape:
-        _refuse(f"{what}: expected {dtype} {tuple(shape)}")
-    n, h, d = t.stride()
-    if d != 1:
-        _refuse(f"{what}: the last dimension must be contiguous")
-    return Strides(0, n, h)
-
-
-def _f32(what: str, t: torch.Tensor, shape) -> int:
-    if t.dtype is not _f32_t or t.shape != shape or not t.is_contiguous():
-        _refuse(f"{what}: expected contiguous float32 {tuple(shape)}")
-    return t.data_ptr()
-
-
-def _bounds(cu: torch.Tensor) -> int:
-    if cu.dim() != 1 or cu.shape[0] < 2:
-        _refuse("cu_seqlens: an int32 vector of at least two bounds")
-    return cu.shape[0] - 1
+def _call(name: str, device_of: torch.Tensor, *args) -> None:
+    """The native call; it declines where another device than its tensors' is current."""
+    f = getattr(_native or _marshal(), name)
+    if not f(*args):
+        with torch.cuda.device(device_of.get_device()):
+            f(*args)
 
 
 @functools.lru_cache(maxsize=256)
-def _head_array(heads: tuple):
-    return (ctypes.c_int32 * len(heads))(*[int(h) for h in heads])
+def _head_bytes(heads: tuple) -> bytes:
+    return struct.pack(f"{len(heads)}i", *[int(h) for h in heads])
 
 
-def _stream(dev: int, stream) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """Scratch that belongs to the stream it is used on, so that its memory is not handed out before the work ends."""
+    dev = like.get_device()
+    if dev < 0:
+        import long_context_hybrid_b200 as base
+        raise base.RtpError("CUDA tensors only")
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _workspace(nbytes: int, dev: int, ws: Optional[torch.Tensor], stream) -> torch.Tensor:
-    if ws is None:
-        return _empty(nbytes, torch.uint8, dev, stream)
-    if ws.get_device() != dev or not ws.is_contiguous():
-        _refuse("ws: a contiguous tensor on the call's device")
-    return ws
-
-
-def _run(name: str, dev: int, *args) -> None:
-    """The C call with its tensors' device current."""
-    if dev == torch._C._cuda_getDevice():
-        status = _fn(name)(*args)
-    else:
-        with torch.cuda.device(dev):
-            status = _fn(name)(*args)
-    if status != 0:
-        import long_context_hybrid_b200 as base
-        base._check(status, name)
+def _bytes(ws: torch.Tensor) -> torch.Tensor:
+    return ws if ws.dtype is torch.uint8 else ws.view(torch.uint8)
 
 
 class PagedCache:
@@ -156,28 +112,28 @@ class PagedCache:
     caller's; the pages they hold are written by ``paged_append`` and
     ``cache_evict``."""
 
+    __slots__ = ("k", "v", "table", "weights", "packed")
+
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, weights: Optional[torch.Tensor] = None):
-        shape, dtype = k.shape, k.dtype
-        if len(shape) != 4 or dtype not in _DTYPES or v.shape != shape or v.dtype is not dtype or shape[3] != _D:
-            _refuse(f"PagedCache: k and v [num_pages, page_size, Hkv, {_D}], bf16 or fp16 alike")
-        kp, kn, kh, kd = k.stride()
-        vp, vn, vh, vd = v.stride()
-        if kd != 1 or vd != 1:
-            _refuse("PagedCache: D must be contiguous")
-        if table.dtype is not _i32_t or table.dim() != 2:
-            _refuse("PagedCache: table int32 [B, max_pages]")
-        B, n = table.shape
-        row, step = table.stride()
-        if n > 1 and step != 1:
-            _refuse("PagedCache: the table's rows must be contiguous")
-        self.dev = _device("PagedCache", k, v, table, weights)
-        P, page, Hkv, _ = shape
-        w = None if weights is None else _f32("PagedCache: weights", weights, (P, Hkv, page))
+        self.packed = (_native or _marshal()).cache(k, v, table, weights)
         self.k, self.v, self.table, self.weights = k, v, table, weights
-        self.num_pages, self.page_size, self.Hkv, self.D, self.dtype = P, page, Hkv, _D, dtype
-        self.B, self.capacity = B, n * page
-        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), Strides(kp, kn, kh), Strides(vp, vn, vh), w,
-                                   table.data_ptr(), row if B > 1 else max(n, 1), P, page, n, Hkv)
+
+    @property
+    def num_pages(self) -> int:
+        return self.k.shape[0]
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def Hkv(self) -> int:
+        return self.k.shape[2]
+
+    @property
+    def capacity(self) -> int:
+        """Slots of a sequence."""
+        return self.table.shape[1] * self.k.shape[1]
 
 
 def attn_packed(q, k, v, o, heads: Sequence[int], cu_seqlens, window: Optional[int] = None,
@@ -187,21 +143,9 @@ def attn_packed(q, k, v, o, heads: Sequence[int], cu_seqlens, window: Optional[i
     ``cu_seqlens`` int32 [S+1] on the device; writes o[:, heads] (rows of
     sequences) and ``lse`` fp32 [len(heads), T]. ``window`` None: the whole
     prefix."""
-    T, Hq, D = shape = q.shape
-    kshape, dtype = k.shape, q.dtype
-    dev = _device("attn_packed", q, k, v, o, cu_seqlens, lse)
-    if dtype not in _DTYPES or D != _D or len(kshape) != 3 or kshape[0] != T or kshape[2] != D:
-        _refuse("attn_packed: q [T, Hq, 128] and k [T, Hkv, 128], bf16 or fp16")
-    S = _bounds(cu_seqlens)
-    heads = _head_array(tuple(heads))
-    n = len(heads)
-    buf = _workspace(256, dev, ws, stream)
-    _run("rtp_attn_packed", dev, q.data_ptr(), _rows("q", q, shape, dtype), k.data_ptr(),
-         _rows("k", k, kshape, dtype), v.data_ptr(), _rows("v", v, kshape, dtype), o.data_ptr(),
-         _rows("o", o, shape, dtype), _DTYPES[dtype], T, Hq, kshape[1], heads, n,
-         _int32("cu_seqlens", cu_seqlens, S + 1), S, _INT32_MAX if window is None else window,
-         _SCALE if scale is None else scale, None if lse is None else _f32("lse", lse, (n, T)), buf.data_ptr(),
-         buf.nbytes, _stream(dev, stream))
+    ws = _empty(256, torch.uint8, q, stream) if ws is None else _bytes(ws)
+    _call("attn_packed", q, q, k, v, o, _head_bytes(tuple(heads)), cu_seqlens, window, scale, lse, ws,
+          None if stream is None else stream.cuda_stream)
     return o
 
 
@@ -212,20 +156,9 @@ def attn_key_weights(q, k, lse, weights, heads: Sequence[int], cu_seqlens, n_obs
     ``n_obs`` rows of its sequence (None: every row), summed over the listed
     heads of its KV head, into ``weights`` fp32 [Hkv, T]; ``lse`` fp32
     [len(heads), T] from ``attn_packed``."""
-    T, Hq, D = shape = q.shape
-    kshape, dtype = k.shape, q.dtype
-    dev = _device("attn_key_weights", q, k, lse, weights, cu_seqlens)
-    if dtype not in _DTYPES or D != _D or len(kshape) != 3 or kshape[0] != T or kshape[2] != D:
-        _refuse("attn_key_weights: q [T, Hq, 128] and k [T, Hkv, 128], bf16 or fp16")
-    S = _bounds(cu_seqlens)
-    heads = _head_array(tuple(heads))
-    n = len(heads)
-    buf = _workspace(256, dev, ws, stream)
-    _run("rtp_attn_key_weights", dev, q.data_ptr(), _rows("q", q, shape, dtype), k.data_ptr(),
-         _rows("k", k, kshape, dtype), _DTYPES[dtype], T, Hq, kshape[1], heads, n,
-         _int32("cu_seqlens", cu_seqlens, S + 1), S, _f32("lse", lse, (n, T)), _INT32_MAX if n_obs is None else n_obs,
-         _INT32_MAX if window is None else window, _SCALE if scale is None else scale,
-         _f32("weights", weights, (kshape[1], T)), buf.data_ptr(), buf.nbytes, _stream(dev, stream))
+    ws = _empty(256, torch.uint8, q, stream) if ws is None else _bytes(ws)
+    _call("attn_key_weights", q, q, k, lse, weights, _head_bytes(tuple(heads)), cu_seqlens, n_obs, window, scale, ws,
+          None if stream is None else stream.cuda_stream)
     return weights
 
 
@@ -234,15 +167,8 @@ def paged_append(cache: PagedCache, k, v, cu_seqlens, pos, weights: Optional[tor
     ``cu_seqlens`` int32 [S+1]) goes to slot pos[i] + t - cu_seqlens[i] of
     table row i. ``weights`` fp32 [Hkv,T] starts their accumulated weights
     (None: 0)."""
-    T = k.shape[0]
-    shape, dtype = (T, cache.Hkv, _D), cache.dtype
-    dev = _device("paged_append", cache.k, k, v, cu_seqlens, pos, weights)
-    S = _bounds(cu_seqlens)
-    if S > cache.B:
-        _refuse("paged_append: more sequences than table rows")
-    _run("rtp_paged_append", dev, cache.struct, k.data_ptr(), _rows("k", k, shape, dtype), v.data_ptr(),
-         _rows("v", v, shape, dtype), None if weights is None else _f32("weights", weights, (cache.Hkv, T)), T,
-         _int32("cu_seqlens", cu_seqlens, S + 1), S, _int32("pos", pos, S), _stream(dev, stream))
+    _call("paged_append", k, cache.packed, k, v, cu_seqlens, pos, weights,
+          None if stream is None else stream.cuda_stream)
 
 
 def paged_attn_decode(q, cache: PagedCache, lens, o, heads: Sequence[int], window: Optional[int] = None,
@@ -254,28 +180,22 @@ def paged_attn_decode(q, cache: PagedCache, lens, o, heads: Sequence[int], windo
     ``max_len`` (default: the table's capacity) bounds the lengths. ``lse``
     fp32 [B,len(heads)]; ``weights_out`` (like cache.weights, may be it)
     receives cache.weights plus this token's attention weights."""
-    B, Hq, _ = q.shape
-    shape, dtype = (B, Hq, _D), cache.dtype
-    dev = _device("paged_attn_decode", cache.k, q, lens, o, lse, weights_out)
-    qs, os_ = _rows("q", q, shape, dtype), _rows("o", o, shape, dtype)
-    qs.b, os_.b = qs.n, os_.n
-    if B > cache.B:
-        _refuse("paged_attn_decode: more sequences than table rows")
-    heads = _head_array(tuple(heads))
-    n = len(heads)
     if max_len is None:
         max_len = cache.capacity
-    if window is None:
-        window = _INT32_MAX
-    w = None
-    if weights_out is not None:
-        w = _f32("weights_out", weights_out, (cache.num_pages, cache.Hkv, cache.page_size))
-    buf = _workspace(_fn("rtp_workspace_size_paged_attn_decode")(B, max_len, n, window, sink, w is not None), dev, ws,
-                     stream)
-    _run("rtp_paged_attn_decode", dev, q.data_ptr(), qs, cache.struct, _int32("lens", lens, B), max_len, o.data_ptr(),
-         os_, _DTYPES[dtype], B, Hq, heads, n, window, sink, _SCALE if scale is None else scale,
-         None if lse is None else _f32("lse", lse, (B, n)), w, buf.data_ptr(), buf.nbytes, _stream(dev, stream))
+    if ws is None:
+        ws = _empty(decode_workspace_size(q.shape[0], max_len, len(heads), window, sink, weights_out is not None),
+                    torch.uint8, q, stream)
+    else:
+        ws = _bytes(ws)
+    _call("paged_attn_decode", q, q, cache.packed, lens, o, _head_bytes(tuple(heads)), window, sink, scale, max_len,
+          lse, weights_out, ws, None if stream is None else stream.cuda_stream)
     return o
+
+
+def decode_workspace_size(B: int, max_len: int, n_heads: int, window: Optional[int], sink: int,
+                          with_weights: bool) -> int:
+    """Bytes of workspace that ``paged_attn_decode`` needs."""
+    return (_native or _marshal()).decode_workspace_size(B, max_len, n_heads, window, sink, with_weights)
 
 
 def cache_evict(cache: PagedCache, lens, budget: int, sink: int = 0, recent: int = 0,
@@ -288,23 +208,12 @@ def cache_evict(cache: PagedCache, lens, budget: int, sink: int = 0, recent: int
     int32 [B])."""
     if out is None:
         out = cache
-    B = lens.shape[0]
-    dev = _device("cache_evict", cache.k, lens, out.k, idx, new_lens)
-    if cache.dtype is not out.dtype:
-        _refuse("cache_evict: caches of different types")
-    if cache.weights is None or out.weights is None:
-        _refuse("cache_evict: both caches need weights")
-    if B > cache.B or B > out.B:
-        _refuse("cache_evict: more sequences than table rows")
     if idx is None:
-        idx = _empty((B, cache.Hkv, budget), _i32_t, dev, stream)
+        idx = _empty((lens.shape[0], cache.Hkv, max(budget, 0)), torch.int32, lens, stream)
     if new_lens is None:
-        new_lens = _empty((B,), _i32_t, dev, stream)
-    if idx.dtype is not _i32_t or idx.shape != (B, cache.Hkv, budget) or not idx.is_contiguous():
-        _refuse(f"idx: expected contiguous int32 {(B, cache.Hkv, budget)}")
-    _run("rtp_cache_evict", dev, cache.struct, out.struct, B, _int32("lens", lens, B),
-         cache.capacity if max_len is None else max_len, budget, sink, recent, idx.data_ptr(),
-         _int32("new_lens", new_lens, B), _stream(dev, stream))
+        new_lens = _empty((lens.shape[0],), torch.int32, lens, stream)
+    _call("cache_evict", lens, cache.packed, out.packed, lens, budget, sink, recent, idx, new_lens,
+          cache.capacity if max_len is None else max_len, None if stream is None else stream.cuda_stream)
     return idx, new_lens
 
 
@@ -326,15 +235,15 @@ class PagedLayer:
         self.streaming = list(streaming)
         self.full = [h for h in range(Hq) if h not in set(self.streaming)]
         if self.streaming and window is None:
-            _refuse("PagedLayer: streaming heads need a window")
+            import long_context_hybrid_b200 as base
+            raise base.RtpError("PagedLayer: streaming heads need a window")
         self.scale = scale
-        B, dev = cache.B, cache.dev
+        B, dev = cache.table.shape[0], cache.k.device
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
         self.cu_decode = torch.arange(B + 1, dtype=torch.int32, device=dev)
         self.ws_prefill = torch.zeros(256, dtype=torch.uint8, device=dev)
         weighed = cache.weights is not None
-        size = _fn("rtp_workspace_size_paged_attn_decode")
-        self.ws = torch.empty(max(size(B, cache.capacity, max(1, len(g)), _INT32_MAX if w is None else w, sink, weighed)
+        self.ws = torch.empty(max(decode_workspace_size(B, cache.capacity, len(g), w, sink, weighed)
                                   for g, w in self._groups()), dtype=torch.uint8, device=dev)
 
     def _groups(self):
@@ -343,7 +252,7 @@ class PagedLayer:
 
     def prefill(self, q, k, v, o, cu_seqlens, stream=None):
         """q/o [T,Hq,D], k/v [T,Hkv,D] of B packed prompts (one per table row)."""
-        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.dev)):
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.k.device)):
             weights = None
             for heads, window in self._groups():
                 lse = None
@@ -362,7 +271,7 @@ class PagedLayer:
 
     def decode(self, q, k, v, o, stream=None):
         """q/o [B,Hq,D], k/v [B,Hkv,D]: one new token of every sequence."""
-        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.dev)):
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.k.device)):
             paged_append(self.cache, k, v, self.cu_decode, self.lens)
             self.lens.add_(1)
             for heads, window in self._groups():
@@ -373,7 +282,7 @@ class PagedLayer:
     def evict(self, budget: int, recent: int, stream=None):
         """Shrinks every sequence to ``budget`` tokens per KV head, keeping the
         ``sink`` first and ``recent`` last; returns the kept slots."""
-        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.dev)):
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.k.device)):
             idx, new_lens = cache_evict(self.cache, self.lens, budget, self.sink, recent)
             self.lens.copy_(new_lens)
         return idx
