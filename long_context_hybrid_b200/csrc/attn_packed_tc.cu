@@ -101,7 +101,7 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
   int c0, n, row0;                                   // the sequence's first row and length, the CTA's first row in it
   // a wait runs out seconds after its block began, long after this
   if (blockIdx.x == 0 && tid == 0) *status = 0;
-  if (!packed_tile(p.cu, p.S, p.T, kTileRows, p.n_numbers - 1 - blockIdx.x / p.n_heads, &c0, &n, &row0)) return;
+  if (!packed_tile<kTileRows>(p.cu, p.S, p.T, p.n_numbers - 1 - blockIdx.x / p.n_heads, &c0, &n, &row0)) return;
 
   // key tiles kt_lo .. kt_lo + n_tiles - 1 (of 128 keys); query tile t takes
   // those of [first[t], last[t]), counted from kt_lo

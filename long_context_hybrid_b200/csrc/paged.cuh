@@ -46,20 +46,25 @@ __device__ __forceinline__ int warp_last_le(F f, int n, int64_t t) {
   return lo + __popc(__ballot_sync(0xffffffffu, lane < n && f(lo + lane) <= t)) - 1;
 }
 
-// Tiles of `rows` query rows of packed sequences without a list: sequence i
-// owns the tile numbers floor(cu[i] / rows) + i .. floor(cu[i+1] / rows) + i,
-// which are at least ceil(len / rows) of them, so floor(T / rows) + S numbers
-// cover any lengths. Finds a number's sequence [c0, c1) (row numbers clamped to
-// [0, T]) and its first row within the sequence; false where there is none.
-__device__ __forceinline__ bool packed_tile(const int32_t* cu, int S, int T, int rows, int64_t number, int* c0,
-                                            int* n, int* row0) {
-  auto at = [&](int x) -> int64_t { return min(max(__ldg(cu + x), 0), T); };
-  const int i = warp_last_le([&](int x) -> int64_t { return at(x) / rows + x; }, S, number);
+// Tiles of kRows (a power of two) rows of packed sequences without a list:
+// sequence i owns the tile numbers floor(cu[i] / kRows) + i .. floor(cu[i+1] /
+// kRows) + i, which are at least ceil(len / kRows) of them, so floor(T / kRows) +
+// S numbers cover any lengths. Finds a number's sequence [c0, c0 + n) (row
+// numbers clamped to [0, T]) and its first row within the sequence; false where
+// there is none.
+template <int kRows>
+__device__ __forceinline__ bool packed_tile(const int32_t* cu, int S, int T, int64_t number, int* c0, int* n,
+                                            int* row0) {
+  static_assert((kRows & (kRows - 1)) == 0, "tiles start at multiples");
+  constexpr int kShift = kRows == 128 ? 7 : 8;
+  static_assert(1 << kShift == kRows, "128 or 256 rows");
+  auto at = [&](int x) -> int { return min(max(__ldg(cu + x), 0), T); };
+  const int i = warp_last_le([&](int x) -> int64_t { return (int64_t)(at(x) >> kShift) + x; }, S, number);
   if (i < 0) return false;
-  const int64_t a = at(i), b = at(i + 1);
-  *c0 = (int)a;
-  *n = (int)(b > a ? b - a : 0);
-  const int64_t r = (number - (a / rows + i)) * rows;
+  const int a = at(i), b = at(i + 1);
+  *c0 = a;
+  *n = b > a ? b - a : 0;
+  const int64_t r = (number - ((a >> kShift) + (int64_t)i)) << kShift;
   *row0 = (int)r;
   return r < *n;
 }

@@ -219,7 +219,10 @@ def test_attn_packed_growing_scores_rescale():
     ([1000, 3], 4, 1, 129, None, [0, 1, 2, 3]),
     ([900], 2, 2, 1, 5, [0, 1]),
     ([2100], 16, 1, None, 1, list(range(16))),
-], ids=lambda c: f"{c[0]}w{c[3]}o{c[4]}")
+    ([700, 64, 1, 0, 65, 1500], 16, 2, None, 64, list(range(16))),
+    ([300, 900, 40], 8, 2, 200, 100, [0, 1, 2, 3, 5, 6]),
+    ([60] * 300, 2, 2, None, 17, [0, 1]),
+], ids=lambda c: f"{c[0][:5]}w{c[3]}o{c[4]}")
 def test_attn_key_weights(case, dtype):
     lens, Hq, Hkv, window, n_obs, heads = case
     (q, k, v), cu, cu_d = make_packed(lens, Hq, Hkv, dtype, 23 + sum(lens), 2, 130, 8)
