@@ -69,7 +69,7 @@ struct PackedParams {
 
 struct Bars {
   uint64_t q_full[2], full[kRing], empty[kRing], v_ok[kRing];
-  uint64_t s_full[2], p_full[2][2], fin;             // p_full[query tile][64-key half]
+  uint64_t s_full[2], p_full[2][2], o_full[2], fin;  // p_full[query tile][64-key half]
   uint32_t tmem_base;
   int abort;
   int poison;                                        // the guard met a non-finite value of the sequence
@@ -123,10 +123,26 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     return k0 + kKeyTile - 1 > row0 || k0 <= row_last - window;
   };
 
+  auto load_q = [&](int t) {
+    const uint32_t bar = smem_u32(&bars.q_full[t]);
+    mbar_arrive_expect_tx(bar, kStage);
+    tma_load_4d(sb + t * kStage, &tmQ, bar, 0, h, c0 + row0 + t * 128, 0);
+    tma_load_4d(sb + t * kStage + 16384, &tmQ, bar, 64, h, c0 + row0 + t * 128, 0);
+  };
+  auto load_kv = [&](int r) {                          // item 2j is K of tile j, 2j + 1 its V
+    const int s = r % kRing;
+    const uint32_t dst = sb + kRingOff + s * kStage, bar = smem_u32(&bars.full[s]);
+    const CUtensorMap* map = (r & 1) ? &tmV : &tmK;
+    const int key = c0 + (kt_lo + (r >> 1)) * kKeyTile;
+    mbar_arrive_expect_tx(bar, kStage);
+    tma_load_4d(dst, map, bar, 0, g, key, 0);
+    tma_load_4d(dst + 16384, map, bar, 64, g, key, 0);
+  };
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&bars.q_full[t]), 1);
       mbar_init(smem_u32(&bars.s_full[t]), 1);
+      mbar_init(smem_u32(&bars.o_full[t]), 1);
       for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&bars.p_full[t][x]), 4);
     }
     for (int s = 0; s < kRing; ++s) {
@@ -138,6 +154,12 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     bars.abort = 0;
     bars.poison = 0;
     fence_mbar_init();
+    // the first copies need nothing else: on their way under the rest of the prologue
+    load_q(0);
+    for (int r = 0; r < min(kRing, 2 * n_tiles); ++r) {
+      load_kv(r);
+      if (r == 0 && last[1] > 0) load_q(1);
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&bars.tmem_base), kTmemCols);
@@ -154,28 +176,11 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
    if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      tma_prefetch(&tmQ);
-      tma_prefetch(&tmK);
-      tma_prefetch(&tmV);
-      auto load_q = [&](int t) {
-        const uint32_t bar = smem_u32(&bars.q_full[t]);
-        mbar_arrive_expect_tx(bar, kStage);
-        tma_load_4d(sb + t * kStage, &tmQ, bar, 0, h, c0 + row0 + t * 128, 0);
-        tma_load_4d(sb + t * kStage + 16384, &tmQ, bar, 64, h, c0 + row0 + t * 128, 0);
-      };
-      load_q(0);
-      int issued = 0;
-      for (int r = 0; r < 2 * n_tiles; ++r) {        // item 2j is K of tile j, 2j + 1 its V
-        const int s = r % kRing;
-        if (r >= kRing && !mbar_wait(smem_u32(&bars.empty[s]), (r / kRing - 1) & 1, abort_flag)) break;
-        const uint32_t dst = sb + kRingOff + s * kStage, bar = smem_u32(&bars.full[s]);
-        const CUtensorMap* map = (r & 1) ? &tmV : &tmK;
-        const int key = c0 + (kt_lo + (r >> 1)) * kKeyTile;
-        mbar_arrive_expect_tx(bar, kStage);
-        tma_load_4d(dst, map, bar, 0, g, key, 0);
-        tma_load_4d(dst + 16384, map, bar, 64, g, key, 0);
+      int issued = min(kRing, 2 * n_tiles);
+      for (int r = kRing; r < 2 * n_tiles; ++r) {
+        if (!mbar_wait(smem_u32(&bars.empty[r % kRing]), (r / kRing - 1) & 1, abort_flag)) break;
+        load_kv(r);
         issued = r + 1;
-        if (r == 0 && last[1] > 0) load_q(1);
       }
       // The MMA side ends every path by committing `fin`; after an abort the
       // copies that nobody consumed are waited for, with a short bound.
@@ -186,7 +191,7 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
       }
       if (*abort_flag) {
         wait_short(smem_u32(&bars.q_full[0]), 0);
-        if (last[1] > 0 && issued > 0) wait_short(smem_u32(&bars.q_full[1]), 0);
+        if (last[1] > 0) wait_short(smem_u32(&bars.q_full[1]), 0);
         for (int r = max(0, issued - kRing); r < issued; ++r)
           wait_short(smem_u32(&bars.full[r % kRing]), (r / kRing) & 1);
       }
@@ -196,15 +201,26 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     const uint32_t on = elect_one();
     const uint64_t q_desc = desc_k_major(sb), k_desc = desc_k_major(sb + kRingOff),
                    v_desc = desc_mn_major(sb + kRingOff);
-    // stage and turn of the K and V item in use
-    int k_st = 0, k_turn = 0, v_st = 1, v_turn = 0;
-    for (int j = -1; j < n_tiles; ++j) {
+    // each tile's first scores (the second's first key tile may be number 1)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (last[t] > first[t]) {
+        mbar_pass(smem_u32(&bars.q_full[t]), 0, abort_flag);
+        mbar_pass(smem_u32(&bars.full[2 * first[t]]), 0, abort_flag);
+        tc_fence_after();
+        issue_qk<F16>(on, t * 256u, q_desc + t * (kStage >> 4), k_desc + (uint64_t)(2 * first[t]) * (kStage >> 4));
+        commit_if(on, smem_u32(&bars.s_full[t]));
+      }
+    }
+    commit_if(on, smem_u32(&bars.empty[0]));
+    // stage and turn of the K item of tile j + 1 and of the V item of tile j
+    int k_st = 2, k_turn = 0, v_st = 1, v_turn = 0;
+    for (int j = 0; j < n_tiles; ++j) {
       const uint64_t v_d = v_desc + (uint64_t)v_st * (kStage >> 4);
       const uint64_t k_d = k_desc + (uint64_t)k_st * (kStage >> 4);
-      if (j >= 0) {
-        mbar_pass(smem_u32(&bars.full[v_st]), v_turn & 1, abort_flag);
-        mbar_pass(smem_u32(&bars.v_ok[v_st]), (v_turn >> 1) & 1, abort_flag);
-      }
+      // v_ok of every tile, so that the guard never falls a ring behind
+      mbar_pass(smem_u32(&bars.full[v_st]), v_turn & 1, abort_flag);
+      mbar_pass(smem_u32(&bars.v_ok[v_st]), (v_turn >> 1) & 1, abort_flag);
       if (j + 1 < n_tiles) mbar_pass(smem_u32(&bars.full[k_st]), k_turn & 1, abort_flag);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -215,19 +231,17 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
             tc_fence_after();
             issue_pv<F16>(on, t * 256u + 128u, t * 256u + half * 32u, v_d, half, half || j > first[t]);
           }
+          if (j + 1 == last[t]) commit_if(on, smem_u32(&bars.o_full[t]));
         }
-        if (j + 1 >= first[t] && j + 1 < last[t]) {
-          if (j + 1 == first[t]) mbar_pass(smem_u32(&bars.q_full[t]), 0, abort_flag);
+        if (j + 1 > first[t] && j + 1 < last[t]) {
           tc_fence_after();
           issue_qk<F16>(on, t * 256u, q_desc + t * (kStage >> 4), k_d);
           commit_if(on, smem_u32(&bars.s_full[t]));
         }
       }
-      if (j >= 0) {
-        commit_if(on, smem_u32(&bars.empty[v_st]));
-        v_st += 2;
-        if (v_st >= kRing) { v_st -= kRing; ++v_turn; }
-      }
+      commit_if(on, smem_u32(&bars.empty[v_st]));
+      v_st += 2;
+      if (v_st >= kRing) { v_st -= kRing; ++v_turn; }
       if (j + 1 < n_tiles) commit_if(on, smem_u32(&bars.empty[k_st]));
       k_st += 2;
       if (k_st >= kRing) { k_st -= kRing; ++k_turn; }
@@ -369,14 +383,18 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
       l_run = s0 + s1;
     }
     if (ok) {
-      const bool w = mbar_wait(smem_u32(&bars.fin), 0, abort_flag);
-      if (__all_sync(0xffffffffu, w) && !*abort_flag) {
+      const bool w = mbar_spin(smem_u32(&bars.o_full[t]), 0, abort_flag);
+      if (__all_sync(0xffffffffu, w && !*abort_flag)) {
         tc_fence_after();
         // a row whose every score was -inf is zero
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
         const bool poison = *reinterpret_cast<volatile int*>(&bars.poison) != 0;
         using T16 = typename Elem16<F16>::T;
-        T16* orow = static_cast<T16*>(p.o) + (int64_t)(c0 + i) * p.o_sn + (int64_t)h * p.o_sh;
+        // Rows go out through shared memory (this warp's 32 rows of the query
+        // tile, which is done with), so that a store covers two rows of 256 bytes
+        // and not 16 bytes of 32 (6500 against 2500 clocks); 16-byte pieces
+        // XOR-swizzled by the row.
+        unsigned char* rows = smem + t * kStage + (warp & 3) * 8192;
 #pragma unroll 1
         for (int c4 = 0; c4 < 4; ++c4) {
           uint32_t o[32];
@@ -408,19 +426,26 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
               }
             }
           }
-          if (i < n) {
-            uint4* dst = reinterpret_cast<uint4*>(orow + c4 * 32);
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-              uint4 w4;
-              w4.x = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 0]), __uint_as_float(o[v4 * 8 + 1]));
-              w4.y = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 2]), __uint_as_float(o[v4 * 8 + 3]));
-              w4.z = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 4]), __uint_as_float(o[v4 * 8 + 5]));
-              w4.w = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 6]), __uint_as_float(o[v4 * 8 + 7]));
-              dst[v4] = w4;
-            }
+          for (int v4 = 0; v4 < 4; ++v4) {
+            uint4 w4;
+            w4.x = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 0]), __uint_as_float(o[v4 * 8 + 1]));
+            w4.y = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 2]), __uint_as_float(o[v4 * 8 + 3]));
+            w4.z = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 4]), __uint_as_float(o[v4 * 8 + 5]));
+            w4.w = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 6]), __uint_as_float(o[v4 * 8 + 7]));
+            *reinterpret_cast<uint4*>(rows + lane * 256 + (((c4 * 4 + v4) ^ (lane & 15)) << 4)) = w4;
           }
           __syncwarp();
+        }
+        {
+          const int i0 = row0 + t * 128 + (warp & 3) * 32;
+          T16* out = static_cast<T16*>(p.o) + (int64_t)(c0 + i0) * p.o_sn + (int64_t)h * p.o_sh + (lane & 15) * 8;
+#pragma unroll 4
+          for (int x = 0; x < 16; ++x) {
+            const int rr = 2 * x + (lane >> 4);
+            const uint4 w4 = *reinterpret_cast<const uint4*>(rows + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
+            if (i0 + rr < n) *reinterpret_cast<uint4*>(out + rr * p.o_sn) = w4;
+          }
         }
         if (p.lse && i < n)
           p.lse[(int64_t)jh * p.T + c0 + i] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
