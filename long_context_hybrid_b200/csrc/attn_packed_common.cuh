@@ -46,10 +46,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Maximum of three, NaN if one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+__device__ __forceinline__ float max3f(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 // mbar_wait without the suspend-time hint: woken sooner (a step of the packed
@@ -104,27 +103,25 @@ __device__ __forceinline__ void mbar_pass(uint32_t bar, uint32_t parity, volatil
   __syncwarp();
 }
 
-// 2^x of a pair on the fp32 pipe, for x <= 127 (smaller than -126: 2^-126):
-// x = n + f with n the nearest integer (added and subtracted 1.5 * 2^23, whose
-// sum also holds n in its low bits), 2^f by a polynomial, n added to the
-// exponent. The polynomial is the degree-4 minimax fit to 2^f in relative error on
-// [-1/2, 1/2] (Remez exchange): off by at most 2.7e-6, 4e-8 in the mean.
-__device__ __forceinline__ uint64_t f2_ex2(uint64_t x) {
-  float x0, x1;
-  f2_split(x, x0, x1);
-  const uint64_t xc = f2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const uint64_t big = f2(12582912.f, 12582912.f), neg_big = f2(-12582912.f, -12582912.f);
-  const uint64_t r = f2_add(xc, big);
-  const uint64_t f = f2_fma(f2_add(r, neg_big), f2(-1.f, -1.f), xc);
-  uint64_t y = f2_fma(f, f2(0.00957010221f, 0.00957010221f), f2(0.0559178591f, 0.0559178591f));
-  y = f2_fma(y, f, f2(0.240247443f, 0.240247443f));
-  y = f2_fma(y, f, f2(0.693121791f, 0.693121791f));
-  y = f2_fma(y, f, f2(0.999999285f, 0.999999285f));
-  float r0, r1, y0, y1;
-  f2_split(r, r0, r1);
-  f2_split(y, y0, y1);
-  return f2(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23)),
-            __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23)));
+// Every thread of the cluster meets; what was written before is visible after.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Address of this CTA's shared-memory address in the CTA of `rank`.
+__device__ __forceinline__ uint32_t remote_smem(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void remote_st1(uint32_t addr, int x) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void remote_st2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void remote_st4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 
 __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity) {

@@ -51,17 +51,21 @@ constexpr uint32_t kStage = 32768;                   // one K or V tile: [D half
 constexpr uint32_t kRingOff = 2 * kStage;            // behind the two Q tiles
 constexpr uint32_t kTmemCols = 512;                  // tile t: S at 256 t, O at 256 t + 128
 constexpr int kStatusTimeout = 4;
-// Every kPolyEvery-th pair of exponentials of an uncut tile goes to the fp32
-// pipe instead of the exponential unit (16 a clock and SM: 1024 clocks a tile of
-// 128 x 128, as long as its two products).
-constexpr int kPolyEvery = 8;
-
+// Few units: the CTAs of a cluster split the key tiles of one. At the end each
+// query tile's partials (64 KB and a maximum and sum a row) go to the CTA whose
+// rank is the tile's number, over distributed shared memory, into the space of
+// the query tiles and the ring.
+constexpr int kMaxRanks = 3;
+constexpr uint32_t kPartial = 65536;
+constexpr uint32_t kMergedRowsOff = (kMaxRanks - 1) * kPartial;       // output rows behind the partials
+constexpr uint32_t kMergedSumsOff = kMergedRowsOff + kStage;          // float2 [rank slot][row]
 struct PackedParams {
   void* o; int64_t o_sn, o_sh;
   const void* v; int64_t v_sn, v_sh;                 // for the epilogue's non-finite values
   const int32_t* cu;
   float* lse;                                        // [n_heads, T] or NULL
   int S, T, G, window, n_heads;
+  int ranks;                                         // CTAs that share a unit's keys (a cluster): 1 to kMaxRanks
   int64_t n_numbers;                                 // tile numbers: floor(T / 256) + S
   float scale_log2;
   uint8_t head[kMaxHeads];
@@ -96,18 +100,20 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
   Bars& bars = *reinterpret_cast<Bars*>(smem + kRingOff + kRing * kStage);
   volatile int* abort_flag = &bars.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int jh = blockIdx.x % p.n_heads;
+  const int ranks = p.ranks, rank = blockIdx.x % ranks, unit = blockIdx.x / ranks;
+  const int jh = unit % p.n_heads;
   const int h = p.head[jh], g = h / p.G;
   int c0, n, row0;                                   // the sequence's first row and length, the CTA's first row in it
   // a wait runs out seconds after its block began, long after this
   if (blockIdx.x == 0 && tid == 0) *status = 0;
-  if (!packed_tile<kTileRows>(p.cu, p.S, p.T, p.n_numbers - 1 - blockIdx.x / p.n_heads, &c0, &n, &row0)) return;
+  if (!packed_tile<kTileRows>(p.cu, p.S, p.T, p.n_numbers - 1 - unit / p.n_heads, &c0, &n, &row0)) return;   // all ranks alike
 
   // key tiles kt_lo .. kt_lo + n_tiles - 1 (of 128 keys); query tile t takes
   // those of [first[t], last[t]), counted from kt_lo
   const int window = p.window;
   int first[2], last[2];
-  const int kt_lo = max(0, row0 - window + 1) / kKeyTile;
+  const int kt_all = max(0, row0 - window + 1) / kKeyTile;
+  int kt_lo = kt_all;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int r = row0 + t * 128;
@@ -115,11 +121,22 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     first[t] = any ? max(0, r - window + 1) / kKeyTile - kt_lo : 0;
     last[t] = any ? min(n - 1, r + 127) / kKeyTile + 1 - kt_lo : 0;
   }
-  const int n_tiles = max(last[0], last[1]);
+  const int n_all = max(last[0], last[1]);
+  int n_tiles = n_all;
+  if (ranks > 1) {                                   // this rank's part of them
+    const int lo = rank * n_all / ranks, hi = (rank + 1) * n_all / ranks;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      first[t] = min(max(first[t], lo), hi) - lo;
+      last[t] = max(min(max(last[t], lo), hi) - lo, first[t]);
+    }
+    kt_lo += lo;
+    n_tiles = hi - lo;
+  }
   const int row_last = min(n - 1, row0 + kTileRows - 1);
   // a tile of which some row of the CTA does not attend some key
-  auto masked = [&](int j) {
-    const int k0 = (kt_lo + j) * kKeyTile;
+  auto masked = [&](int kt) {
+    const int k0 = kt * kKeyTile;
     return k0 + kKeyTile - 1 > row0 || k0 <= row_last - window;
   };
 
@@ -155,10 +172,10 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     bars.poison = 0;
     fence_mbar_init();
     // the first copies need nothing else: on their way under the rest of the prologue
-    load_q(0);
+    if (last[0] > first[0]) load_q(0);
     for (int r = 0; r < min(kRing, 2 * n_tiles); ++r) {
       load_kv(r);
-      if (r == 0 && last[1] > 0) load_q(1);
+      if (r == 0 && last[1] > first[1]) load_q(1);
     }
   }
   if (warp == 1) {
@@ -190,8 +207,8 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
         }
       }
       if (*abort_flag) {
-        wait_short(smem_u32(&bars.q_full[0]), 0);
-        if (last[1] > 0) wait_short(smem_u32(&bars.q_full[1]), 0);
+        if (last[0] > first[0]) wait_short(smem_u32(&bars.q_full[0]), 0);
+        if (last[1] > first[1]) wait_short(smem_u32(&bars.q_full[1]), 0);
         for (int r = max(0, issued - kRing); r < issued; ++r)
           wait_short(smem_u32(&bars.full[r % kRing]), (r / kRing) & 1);
       }
@@ -212,7 +229,7 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
         commit_if(on, smem_u32(&bars.s_full[t]));
       }
     }
-    commit_if(on, smem_u32(&bars.empty[0]));
+    if (n_tiles > 0) commit_if(on, smem_u32(&bars.empty[0]));
     // stage and turn of the K item of tile j + 1 and of the V item of tile j
     int k_st = 2, k_turn = 0, v_st = 1, v_turn = 0;
     for (int j = 0; j < n_tiles; ++j) {
@@ -259,7 +276,7 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
       const bool w = mbar_spin(smem_u32(&bars.full[s]), (r / kRing) & 1, abort_flag);
       if (!__all_sync(0xffffffffu, w)) break;
       if (!(r & 1)) continue;
-      if (masked(j)) {
+      if (masked(kt_lo + j)) {
         uint4* tile = reinterpret_cast<uint4*>(smem + kRingOff + s * kStage);
         const int there = n - (kt_lo + j) * kKeyTile;     // rows of the tile that are keys of the sequence
         bool met = false;
@@ -281,6 +298,10 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
       }
       if (lane == 0) mbar_arrive(smem_u32(&bars.v_ok[s]));
     }
+   }
+   if (ranks > 1) {                                  // as the softmax warps below
+    cluster_meet();
+    cluster_meet();
    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -321,11 +342,9 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
 #pragma unroll
           for (int c = half * 64; c < half * 64 + 64; c += 2)
             top[(c >> 1) & 3] =
-                max3_nan(top[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                max3f(top[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
         }
-        const float m_cand = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]) * sl2;
-        // a NaN or +inf among the scores makes the whole row NaN
-        if (!(m_cand < INFINITY)) sum = f2(NAN, NAN);
+        const float m_cand = max3f(max3f(top[0], top[1], top[2]), top[3], top[3]) * sl2;
         const bool need = m_cand > m_run + 8.f;
         const float f = need ? ex2(m_run - m_cand) : 1.f;     // 0 while nothing was attended yet
         if (need) m_run = m_cand;
@@ -340,15 +359,9 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
           for (int c = 0; c < 32; ++c) {
             const int at = half * 64 + 2 * c;
             const uint64_t x = f2_fma(f2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), sc2, nb2);
-            float p0, p1;
-            if (!kCut && c % kPolyEvery == kPolyEvery - 1) {
-              f2_split(f2_ex2(x), p0, p1);
-            } else {
-              float x0, x1;
-              f2_split(x, x0, x1);
-              p0 = ex2(x0);
-              p1 = ex2(x1);
-            }
+            float x0, x1;
+            f2_split(x, x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
             sum = f2_add(sum, f2(p0, p1));
             pk[c] = Elem16<F16>::pack(p0, p1);
           }
@@ -382,74 +395,135 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
       f2_split(sum, s0, s1);
       l_run = s0 + s1;
     }
-    if (ok) {
-      const bool w = mbar_spin(smem_u32(&bars.o_full[t]), 0, abort_flag);
-      if (__all_sync(0xffffffffu, w && !*abort_flag)) {
-        tc_fence_after();
-        // a row whose every score was -inf is zero
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-        const bool poison = *reinterpret_cast<volatile int*>(&bars.poison) != 0;
-        using T16 = typename Elem16<F16>::T;
-        // Rows go out through shared memory (this warp's 32 rows of the query
-        // tile, which is done with), so that a store covers two rows of 256 bytes
-        // and not 16 bytes of 32 (6500 against 2500 clocks); 16-byte pieces
-        // XOR-swizzled by the row.
-        unsigned char* rows = smem + t * kStage + (warp & 3) * 8192;
+    // Scales the row's sum of P V, of this CTA and (kMerged) the other ranks'
+    // partials in their order, and writes it and its lse.
+    using T16 = typename Elem16<F16>::T;
+    auto write_out = [&](auto merged, bool poison) {
+      constexpr bool kMerged = decltype(merged)::value;
+      float m_all = m_run, l_all = l_run, f_own = 1.f, f_other[kMaxRanks - 1];
+      const float2* sums = reinterpret_cast<const float2*>(smem + kMergedSumsOff);
+      if (kMerged) {
+#pragma unroll
+        for (int x = 0; x < kMaxRanks - 1; ++x)
+          if (x < ranks - 1) m_all = fmaxf(m_all, sums[x * 128 + r].x);
+        f_own = l_run == 0.f ? 0.f : ex2(m_run - m_all);
+        l_all = l_run * f_own;
+#pragma unroll
+        for (int x = 0; x < kMaxRanks - 1; ++x) {
+          const float2 y = x < ranks - 1 ? sums[x * 128 + r] : make_float2(0.f, 0.f);
+          f_other[x] = y.y == 0.f ? 0.f : ex2(y.x - m_all);
+          l_all += y.y == 0.f ? 0.f : y.y * f_other[x];
+        }
+      }
+      // a row whose every score was -inf is zero
+      const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+      // Rows go out through shared memory (this warp's 32 rows; the query tile is
+      // done with), so that a store covers two rows of 256 bytes and not 16 bytes
+      // of 32 (6500 against 2500 clocks); 16-byte pieces XOR-swizzled by the row.
+      unsigned char* rows = smem + (kMerged ? kMergedRowsOff : t * kStage) + (warp & 3) * 8192;
 #pragma unroll 1
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + c4 * 32u, o);
-          tc_wait_ld();
+      for (int c4 = 0; c4 < 4; ++c4) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + c4 * 32u, o);
+        tc_wait_ld();
+        if (kMerged) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
-          if (poison && i < n) {
-            // what the guard took out, back into this row if it attends the key
-            for (int j = j0; j < j1; ++j) {
-              if (!masked(j)) continue;
-              const int k0 = (kt_lo + j) * kKeyTile;
-              for (int u = max(k0, i - window + 1); u <= min(i, k0 + kKeyTile - 1); ++u) {
-                const uint4* vrow = reinterpret_cast<const uint4*>(
-                    static_cast<const T16*>(p.v) + (int64_t)(c0 + u) * p.v_sn + (int64_t)g * p.v_sh + c4 * 32);
+          for (int c = 0; c < 32; ++c) o[c] = l_run == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * f_own);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  const uint4 d = __ldg(vrow + x);
-                  const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
+          for (int x = 0; x < kMaxRanks - 1; ++x) {
+            if (x >= ranks - 1 || f_other[x] == 0.f) continue;       // nothing was written there
+            const float4* part = reinterpret_cast<const float4*>(smem + x * kPartial) + c4 * 8 * 128 + r;
 #pragma unroll
-                  for (int y = 0; y < 4; ++y) {
-                    const uint32_t bad = nonfinite_bits<F16>(wd[y]);
-                    const int at = x * 8 + y * 2;
-                    if (bad & 0x8000u) o[at] = __float_as_uint(__uint_as_float(o[at]) + Elem16<F16>::lo(wd[y]));
-                    if (bad & 0x80000000u)
-                      o[at + 1] = __float_as_uint(__uint_as_float(o[at + 1]) + Elem16<F16>::hi(wd[y]));
-                  }
+            for (int c = 0; c < 8; ++c) {
+              const float4 y = part[c * 128];
+              o[4 * c] = __float_as_uint(__uint_as_float(o[4 * c]) + f_other[x] * y.x);
+              o[4 * c + 1] = __float_as_uint(__uint_as_float(o[4 * c + 1]) + f_other[x] * y.y);
+              o[4 * c + 2] = __float_as_uint(__uint_as_float(o[4 * c + 2]) + f_other[x] * y.z);
+              o[4 * c + 3] = __float_as_uint(__uint_as_float(o[4 * c + 3]) + f_other[x] * y.w);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+        if (poison && i < n) {
+          // what the guards took out, back into this row if it attends the key
+          for (int kt = kt_all; kt < kt_all + n_all; ++kt) {
+            if (!masked(kt)) continue;
+            const int k0 = kt * kKeyTile;
+            for (int u = max(k0, i - window + 1); u <= min(i, k0 + kKeyTile - 1); ++u) {
+              const uint4* vrow = reinterpret_cast<const uint4*>(
+                  static_cast<const T16*>(p.v) + (int64_t)(c0 + u) * p.v_sn + (int64_t)g * p.v_sh + c4 * 32);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint4 d = __ldg(vrow + x);
+                const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const uint32_t bad = nonfinite_bits<F16>(wd[y]);
+                  const int at = x * 8 + y * 2;
+                  if (bad & 0x8000u) o[at] = __float_as_uint(__uint_as_float(o[at]) + Elem16<F16>::lo(wd[y]));
+                  if (bad & 0x80000000u)
+                    o[at + 1] = __float_as_uint(__uint_as_float(o[at + 1]) + Elem16<F16>::hi(wd[y]));
                 }
               }
             }
           }
+        }
 #pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4) {
-            uint4 w4;
-            w4.x = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 0]), __uint_as_float(o[v4 * 8 + 1]));
-            w4.y = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 2]), __uint_as_float(o[v4 * 8 + 3]));
-            w4.z = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 4]), __uint_as_float(o[v4 * 8 + 5]));
-            w4.w = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 6]), __uint_as_float(o[v4 * 8 + 7]));
-            *reinterpret_cast<uint4*>(rows + lane * 256 + (((c4 * 4 + v4) ^ (lane & 15)) << 4)) = w4;
-          }
-          __syncwarp();
+        for (int v4 = 0; v4 < 4; ++v4) {
+          uint4 w4;
+          w4.x = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 0]), __uint_as_float(o[v4 * 8 + 1]));
+          w4.y = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 2]), __uint_as_float(o[v4 * 8 + 3]));
+          w4.z = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 4]), __uint_as_float(o[v4 * 8 + 5]));
+          w4.w = Elem16<F16>::pack(__uint_as_float(o[v4 * 8 + 6]), __uint_as_float(o[v4 * 8 + 7]));
+          *reinterpret_cast<uint4*>(rows + lane * 256 + (((c4 * 4 + v4) ^ (lane & 15)) << 4)) = w4;
         }
-        {
-          const int i0 = row0 + t * 128 + (warp & 3) * 32;
-          T16* out = static_cast<T16*>(p.o) + (int64_t)(c0 + i0) * p.o_sn + (int64_t)h * p.o_sh + (lane & 15) * 8;
-#pragma unroll 4
-          for (int x = 0; x < 16; ++x) {
-            const int rr = 2 * x + (lane >> 4);
-            const uint4 w4 = *reinterpret_cast<const uint4*>(rows + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
-            if (i0 + rr < n) *reinterpret_cast<uint4*>(out + rr * p.o_sn) = w4;
-          }
-        }
-        if (p.lse && i < n)
-          p.lse[(int64_t)jh * p.T + c0 + i] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+        __syncwarp();
       }
+      const int i0 = row0 + t * 128 + (warp & 3) * 32;
+      T16* out = static_cast<T16*>(p.o) + (int64_t)(c0 + i0) * p.o_sn + (int64_t)h * p.o_sh + (lane & 15) * 8;
+#pragma unroll 4
+      for (int x = 0; x < 16; ++x) {
+        const int rr = 2 * x + (lane >> 4);
+        const uint4 w4 = *reinterpret_cast<const uint4*>(rows + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
+        if (i0 + rr < n) *reinterpret_cast<uint4*>(out + rr * p.o_sn) = w4;
+      }
+      if (p.lse && i < n)
+        p.lse[(int64_t)jh * p.T + c0 + i] = l_all == 0.f ? -INFINITY : (m_all + log2f(l_all)) * 0.69314718055994531f;
+    };
+
+    const bool here = j1 > j0;                       // this CTA has a part of the tile
+    if (here) {
+      const bool w = ok && mbar_spin(smem_u32(&bars.o_full[t]), 0, abort_flag);
+      ok = __all_sync(0xffffffffu, w && !*abort_flag);
+      tc_fence_after();
+    }
+    volatile int* poison = &bars.poison;
+    if (ranks == 1) {
+      if (here && ok) write_out(std::false_type{}, *poison != 0);
+    } else {
+      cluster_meet();                                // nobody's query tiles and ring are in use any more
+      const bool whole = ok || !here;
+      if (rank != t && whole && row0 + t * 128 < n) {
+        const uint32_t slot = rank < t ? rank : rank - 1;
+        const uint32_t to = remote_smem(sb, t);
+        remote_st2(to + kMergedSumsOff + (slot * 128 + r) * 8u, m_run, l_run);
+        if (*poison) remote_st1(remote_smem(smem_u32(&bars.poison), t), 1);
+        if (here) {
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c4 * 32u, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              remote_st4(to + slot * kPartial + ((c4 * 8 + c) * 128 + r) * 16u, o[4 * c], o[4 * c + 1], o[4 * c + 2],
+                         o[4 * c + 3]);
+          }
+        }
+      }
+      cluster_meet();
+      if (rank == t && whole && row0 + t * 128 < n) write_out(std::true_type{}, *poison != 0);
     }
   }
 
@@ -469,8 +543,19 @@ static cudaError_t launch_typed(const PackedParams& p, const CUtensorMap& tq, co
   cudaError_t e =
       cudaFuncSetAttribute(attn_packed_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  attn_packed_kernel<F16><<<(unsigned)(p.n_numbers * p.n_heads), kThreads, kSmemBytes, stream>>>(p, tq, tk, tv, status);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.n_numbers * p.n_heads * p.ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.ranks > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_packed_kernel<F16>, p, tq, tk, tv, status);
 }
 
 cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4& v, void* o, int64_t o_sn,
@@ -488,6 +573,9 @@ cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4
   p.cu = cu; p.lse = lse;
   p.S = S; p.T = T; p.G = Hq / Hkv; p.window = window; p.n_heads = n_heads;
   p.n_numbers = (int64_t)T / kTileRows + S;
+  // few units leave SMs idle: up to three CTAs share one's keys
+  const int64_t units = p.n_numbers * n_heads;
+  p.ranks = units * 3 <= 148 ? 3 : (units * 2 <= 148 ? 2 : 1);
   p.scale_log2 = scale * 1.4426950408889634f;
   for (int j = 0; j < n_heads; ++j) p.head[j] = (uint8_t)heads[j];
   return f16 ? launch_typed<true>(p, tq, tk, tv, status, stream) : launch_typed<false>(p, tq, tk, tv, status, stream);

@@ -104,6 +104,11 @@ PACKED = [
     ([1000], 2, 1, 129, [0, 1], 9, 9, 0),
     ([640, 300], 4, 2, 128, [1, 3], 0, 0, 0),
     ([1500, 1, 64], 16, 1, None, [0, 15], 0, 0, 0),
+    # enough tiles that every CTA has its keys to itself; that two share them (fewer: three)
+    ([700, 65, 0, 300, 1, 129], 32, 4, None, list(range(32)), 0, 3, 0),
+    ([700, 65, 0, 300, 1, 129], 32, 4, 100, list(range(32)), 1, 0, 0),
+    ([600, 300, 500], 8, 2, None, list(range(8)), 0, 0, 8),
+    ([600, 300, 500], 8, 2, 129, list(range(8)), 0, 0, 0),
 ]
 
 
@@ -136,13 +141,15 @@ def test_attn_packed(case, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("window", [None, 40, 200])
-def test_attn_packed_unattended_values_do_not_matter(dtype, window):
+@pytest.mark.parametrize("Hq", [4, 12, 32])       # three CTAs, two, and one to a tile's keys
+def test_attn_packed_unattended_values_do_not_matter(dtype, window, Hq):
     """NaN and infinities in keys and values reach exactly the rows that attend
     them: not the neighbour sequence, not earlier rows, not rows whose window
     has passed."""
     lens = [150, 300, 90]
-    (q, k, v), cu, cu_d = make_packed(lens, 4, 2, dtype, 5)
-    heads = [0, 1, 2, 3]
+    (q, k, v), cu, cu_d = make_packed(lens, Hq, 2, dtype, 5)
+    heads = list(range(Hq))
+    G = Hq // 2
 
     def run():
         o = torch.zeros_like(q)
@@ -161,18 +168,14 @@ def test_attn_packed_unattended_values_do_not_matter(dtype, window):
     hit_v = torch.zeros(T, dtype=torch.bool)
     for row in at:
         hit_v |= reach(row)
-    expect = torch.isfinite(torch.ones(T, 4, D))
-    expect[hit_v, :2, 17] = False
-    expect[reach(400)][:, 2:] = False
     fin = torch.isfinite(got)
-    fine = torch.ones(T, 4, D, dtype=torch.bool)
-    fine[hit_v, :2, 17] = False
-    rk = reach(400)
-    fine[rk, 2:] = False
+    fine = torch.ones(T, Hq, D, dtype=torch.bool)
+    fine[hit_v, :G, 17] = False
+    fine[reach(400), G:] = False
     assert torch.equal(fin, fine)
     assert torch.equal(got[fin], clean[fin])
     only_inf = reach(449) & ~reach(290) & ~reach(153)
-    assert (got[only_inf][:, :2, 17] == float("inf")).all()
+    assert (got[only_inf][:, :G, 17] == float("inf")).all()
 
 
 def test_attn_packed_long_prompt_sampled_rows():
