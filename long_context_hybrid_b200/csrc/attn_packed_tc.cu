@@ -558,6 +558,32 @@ static cudaError_t launch_typed(const PackedParams& p, const CUtensorMap& tq, co
   return cudaLaunchKernelEx(&cfg, attn_packed_kernel<F16>, p, tq, tk, tv, status);
 }
 
+// How many CTAs share a unit's keys, from what the host knows: the units and
+// the mean length. In key tiles' time: alone the call takes as long as its
+// longest unit or its share of all, `work`, whichever is more; split by r the
+// longest unit shrinks, but handing the parts over costs about 2 and every CTA
+// about 4 (2 alone) for its beginning and end. Three only while all CTAs run
+// at once. Measured, alone against by 2 (by 3): one prompt of 8192 tokens, 4 heads
+// 122 against 75 us (98); 4096, 8 heads 65, 51; 2048, 8 heads 37, 26 (34); 2048, 16
+// heads 38, 38; 1024, 32 heads 24, 32; 100 tokens, 8 heads 8, 11.
+static int choose_ranks(int64_t units, int mean_len, int window) {
+  const bool cut = window < mean_len;
+  const double longest = ((cut ? (double)window + kTileRows : mean_len) + kKeyTile - 1) / kKeyTile;
+  const double work = units * (cut ? longest : (longest + 1) / 2) / 148.0;
+  int best = 1;
+  double least = 0;
+  for (int r = 1; r <= kMaxRanks; ++r) {
+    if (r > 2 && units * r > 148) break;
+    const double alone = longest / r + (r > 1 ? 2 : 0), share = work + units * r * (r > 1 ? 4 : 2) / 148.0;
+    const double time = alone > share ? alone : share;
+    if (r == 1 || time < 0.9 * least) {
+      best = r;
+      least = time;
+    }
+  }
+  return best;
+}
+
 cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4& v, void* o, int64_t o_sn,
                                int64_t o_sh, bool f16, int T, int Hq, int Hkv, const int32_t* heads, int n_heads,
                                const int32_t* cu, int S, int window, float scale, float* lse, int* status,
@@ -573,9 +599,7 @@ cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4
   p.cu = cu; p.lse = lse;
   p.S = S; p.T = T; p.G = Hq / Hkv; p.window = window; p.n_heads = n_heads;
   p.n_numbers = (int64_t)T / kTileRows + S;
-  // few units leave SMs idle: up to three CTAs share one's keys
-  const int64_t units = p.n_numbers * n_heads;
-  p.ranks = units * 3 <= 148 ? 3 : (units * 2 <= 148 ? 2 : 1);
+  p.ranks = choose_ranks(p.n_numbers * n_heads, T / S, window);
   p.scale_log2 = scale * 1.4426950408889634f;
   for (int j = 0; j < n_heads; ++j) p.head[j] = (uint8_t)heads[j];
   return f16 ? launch_typed<true>(p, tq, tk, tv, status, stream) : launch_typed<false>(p, tq, tk, tv, status, stream);
