@@ -632,31 +632,26 @@ paged_weights_kernel(const __grid_constant__ DecodeParams p) {
     const Span s = span_of(p, b);
     const int u = block * kWeightThreads + threadIdx.x;
     const int page = u < s.len ? page_of(p.c, b, u) : -1;
-    if (page >= 0) {
-      const int g = p.ag_kv[a], n = p.ag_n[a], j0 = p.ag_start[a];
-      const int64_t w = (((int64_t)page * p.c.Hkv + g) << p.c.page_shift) + (u & ((1 << p.c.page_shift) - 1));
-      const float before = p.c.w[w];
-      if (x == x0) pdl_wait();
-      float sum = 0.f;
-      const int e = u < s.sink ? u : (u >= s.lo ? u - s.lo + s.sink : -1);
-      if (e >= 0) {
-        const float* at = p.logits + ((int64_t)b * p.n_heads + j0) * p.att_cap + e;
-        const float* lse2 = p.lse2 + (int64_t)b * p.n_heads + j0;
-        constexpr int kAhead = 8;             // scores a thread keeps in flight
-        for (int r0 = 0; r0 < n; r0 += kAhead) {
-          float x_[kAhead], l_[kAhead];
+    const int g = p.ag_kv[a], n = p.ag_n[a], j0 = p.ag_start[a];
+    const int64_t w = (((int64_t)max(page, 0) * p.c.Hkv + g) << p.c.page_shift) + (u & ((1 << p.c.page_shift) - 1));
+    const float before = p.c.w[w];            // of page 0 where there is none: loads stay unconditional
+    if (x == x0) pdl_wait();
+    const int e = u < s.sink ? u : (u >= s.lo ? u - s.lo + s.sink : -1);
+    const float* at = p.logits + ((int64_t)b * p.n_heads + j0) * p.att_cap + max(min(e, s.n - 1), 0);
+    const float* lse2 = p.lse2 + (int64_t)b * p.n_heads + j0;
+    float sum = 0.f;
+    constexpr int kAhead = 8;                 // scores a thread keeps in flight
+    for (int r0 = 0; r0 < n; r0 += kAhead) {
+      float x_[kAhead], l_[kAhead];
 #pragma unroll
-          for (int r = 0; r < kAhead; ++r) {
-            x_[r] = r0 + r < n ? at[(r0 + r) * p.att_cap] : -INFINITY;
-            l_[r] = r0 + r < n ? lse2[r0 + r] : 0.f;
-          }
-#pragma unroll
-          for (int r = 0; r < kAhead; ++r) sum += l_[r] == -INFINITY ? 0.f : exp2f(x_[r] - l_[r]);
-        }
+      for (int r = 0; r < kAhead; ++r) {
+        x_[r] = at[min(r0 + r, n - 1) * p.att_cap];
+        l_[r] = lse2[min(r0 + r, n - 1)];
       }
-      p.w_out[w] = before + sum;
+#pragma unroll
+      for (int r = 0; r < kAhead; ++r) sum += r0 + r >= n || l_[r] == -INFINITY ? 0.f : exp2f(x_[r] - l_[r]);
     }
-    if (x == x0) pdl_wait();                  // the threads without a slot in the first block, too
+    if (page >= 0) p.w_out[w] = before + (e >= 0 ? sum : 0.f);
     if (++block == nc && x + 1 < x1) {
       block = 0;
       if (++a == p.n_ag) {

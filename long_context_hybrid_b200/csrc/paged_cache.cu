@@ -1,7 +1,7 @@
 // The paged cache: filling it and shrinking it.
 //
 // rtp_paged_append copies packed K/V rows (and weights) to their slots; it
-// moves 1 KB per token and KV head and is bound by HBM. A CTA takes up to 32
+// moves 1 KB per token and KV head and is bound by HBM. A CTA takes up to 16
 // consecutive tokens: one warp finds their sequences, pages and rows (a lane
 // each), then the warps copy whole rows in 16-byte pieces.
 //
@@ -31,9 +31,11 @@ namespace {
 // ---------------------------------------------------------------------------
 // Append
 // ---------------------------------------------------------------------------
-constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 32;              // most tokens of one CTA: one per lane
-constexpr int kAppendAhead = 8;                // rows a warp keeps in flight
+// 26477 tokens of 4 heads: 22.6 us; 32 tokens, 8 rows, 256 threads 24.6; 8, 8, 256 33.0
+constexpr int kAppendThreads = 128;
+constexpr int kAppendTokens = 16;              // most tokens of one CTA: a lane each
+constexpr int kAppendAhead = 4;                // rows a warp keeps in flight
+static_assert(kAppendTokens <= 32, "a lane finds a token's slot");
 
 struct AppendParams {
   PagedView c;
@@ -63,8 +65,10 @@ paged_append_kernel(const AppendParams p) {
         row = (int)(slot & ((1 << p.c.page_shift) - 1));
       }
     }
-    s_page[lane] = page;
-    s_row[lane] = row;
+    if (lane < n) {
+      s_page[lane] = page;
+      s_row[lane] = row;
+    }
   }
   __syncthreads();
   // a warp moves whole rows: lanes 0..15 the K row, 16..31 the V row of one
@@ -342,7 +346,7 @@ evict_select_kernel(const EvictParams p, int n_keys) {
 // ---------------------------------------------------------------------------
 // Eviction: the move
 // ---------------------------------------------------------------------------
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;
 
 // Out of place: a warp moves whole rows (lanes 0..15 the K row, 16..31 the V
 // row), kMoveRows of them with all loads in flight.
@@ -475,8 +479,7 @@ cudaError_t launch_paged_append(const PagedView& c, const void* k, int64_t k_sn,
   p.v = static_cast<const char*>(v); p.v_sn = v_sn * 2; p.v_sh = v_sh * 2;
   p.w = w; p.w_sh = T;
   p.cu = cu; p.pos = pos; p.S = S; p.T = T;
-  // few tokens spread over the SMs; many share a CTA and its search (8 a CTA: 25 us
-  // for 26477 tokens of 4 heads)
+  // few tokens spread over the SMs; many share a CTA and its search
   p.per_cta = T / 148 < 1 ? 1 : (T / 148 < kAppendTokens ? T / 148 : kAppendTokens);
   paged_append_kernel<<<(T + p.per_cta - 1) / p.per_cta, kAppendThreads, 0, stream>>>(p);
   return cudaGetLastError();
