@@ -26,12 +26,18 @@
 //     segment that lies within one run is finished there; otherwise the CTA
 //     leaves one partial (a run has at most two: its first and its last
 //     segment), and a second kernel joins the partials of each cut segment.
+//   * Short batches (each segment a few chunks a CTA) take one kernel: the
+//     CTAs of a cluster share a segment and join over distributed shared
+//     memory, each writing every n-th row.
 //   * With weights, the first kernel also stores the scaled scores (fp32, 4
 //     bytes against 512 / G per key and head) and a third kernel adds
 //     exp(score - lse) over the heads of a group, in a fixed order.
+#include <cooperative_groups.h>
+
 #include "paged.cuh"
 
 namespace rtp {
+namespace cg = cooperative_groups;
 
 namespace {
 constexpr int kWarps = 4;
@@ -44,6 +50,7 @@ constexpr int kStages = 3;
 constexpr int kSegCost = 3;
 constexpr int kRowBytes = RTP_D * 2;
 constexpr int kSlab = kKeys * kRowBytes;      // one warp's K (or V) rows of one chunk
+constexpr int kMaxRanks = 8;                  // CTAs of a cluster that share a segment
 constexpr int kGroup = 16;                    // query heads per KV head: rows of the tile
 constexpr int kPart = 4 + RTP_D;              // m, l, 2 pad, o[128]
 constexpr size_t kHeaderBytes = 256;          // status word
@@ -56,6 +63,7 @@ struct DecodeParams {
   int B, max_len, window, sink;
   float scale_log2;
   int n_heads, n_ag, rows;                    // listed heads, KV heads with one, most rows of one
+  int ranks;                                  // CTAs that share a segment; 0: the batch's list is cut into runs
   float* part;                                // [2 * CTAs, rows, kPart]
   float* lse;                                 // caller's [B, n_heads] (natural log) or NULL
   float* lse2;                                // [B, n_heads], log2 domain (with weights)
@@ -157,6 +165,7 @@ struct Cursor {
   int64_t unit;                               // of the current chunk; INT64_MAX past the last
   int b, a, local, nc;
   Span s;
+  __device__ Cursor() {}
   __device__ Cursor(const DecodeParams& p, const Place& at, int64_t x) {
     b = at.b;
     nc = at.nc;
@@ -166,6 +175,11 @@ struct Cursor {
     const int rem = (int)(into - (int64_t)a * units_of(nc));
     local = rem > kSegCost ? rem - kSegCost : 0;
     unit = rem > kSegCost ? x : x + (kSegCost - rem);
+  }
+  // chunks [lo, ..) of segment (b, a), a unit each
+  __device__ Cursor(const DecodeParams& p, int b_, int a_, int lo) : unit(lo), b(b_), a(a_), local(lo) {
+    nc = chunks_of(p, b);
+    s = span_of(p, b);
   }
   __device__ void next(const DecodeParams& p) {
     ++unit;
@@ -252,20 +266,36 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;
   if (blockIdx.x == 0 && tid == 0) *p.status = 0;
-  ChunkScan lens(p, sm.scan);
-  const int64_t n_list = lens.total * p.n_ag;
-  const int n_ctas = (int)(n_list < gridDim.x ? n_list : gridDim.x);
-  // sequences that attend nothing
-  for (int x = blockIdx.x * kWarps + warp; x < p.B * p.n_heads; x += gridDim.x * kWarps) {
-    const int b = x / p.n_heads;
-    if (chunks_of(p, b) == 0) write_row<F16>(p, b, x - b * p.n_heads, 0.f, 0.f, make_float4(0, 0, 0, 0), lane);
+  int64_t x1;                                 // end of this CTA's chunks, in units
+  Cursor cur;                                 // chunk being computed
+  if (p.ranks > 0) {
+    const int seg = blockIdx.x / p.ranks, rank = blockIdx.x - seg * p.ranks;
+    const int b = seg / p.n_ag, a = seg - b * p.n_ag;
+    const int nc = chunks_of(p, b);
+    if (nc == 0) {                            // nothing to attend (the same for the whole cluster)
+      for (int r = rank * kWarps + warp; r < p.ag_n[a]; r += p.ranks * kWarps)
+        write_row<F16>(p, b, p.ag_start[a] + r, 0.f, 0.f, make_float4(0, 0, 0, 0), lane);
+      return;
+    }
+    cur = Cursor(p, b, a, rank * nc / p.ranks);
+    x1 = (rank + 1) * nc / p.ranks;
+  } else {
+    ChunkScan lens(p, sm.scan);
+    const int64_t n_list = lens.total * p.n_ag;
+    const int n_ctas = (int)(n_list < gridDim.x ? n_list : gridDim.x);
+    // sequences that attend nothing
+    for (int x = blockIdx.x * kWarps + warp; x < p.B * p.n_heads; x += gridDim.x * kWarps) {
+      const int b = x / p.n_heads;
+      if (chunks_of(p, b) == 0) write_row<F16>(p, b, x - b * p.n_heads, 0.f, 0.f, make_float4(0, 0, 0, 0), lane);
+    }
+    if ((int)blockIdx.x >= n_ctas) return;
+    const int64_t x0 = run_start(blockIdx.x, n_list, n_ctas);
+    x1 = run_start(blockIdx.x + 1, n_list, n_ctas);
+    Place& place = *reinterpret_cast<Place*>(sm.place);
+    lens.locate(p, x0, sm.scan, &place);
+    cur = Cursor(p, place, x0);
+    if (cur.unit >= x1) return;
   }
-  if ((int)blockIdx.x >= n_ctas) return;
-  const int64_t x0 = run_start(blockIdx.x, n_list, n_ctas), x1 = run_start(blockIdx.x + 1, n_list, n_ctas);
-  Place& place = *reinterpret_cast<Place*>(sm.place);
-  lens.locate(p, x0, sm.scan, &place);
-  Cursor cur(p, place, x0);                   // chunk being computed
-  if (cur.unit >= x1) return;
 
   // this warp's ring and its copies of a chunk into stage st
   const uint32_t ring = su32(sm.ring[warp]);
@@ -276,7 +306,7 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
     slot = icur.slot(icur.local * kChunk + my_key);
     return slot < 0 ? -1 : page_of(p.c, icur.b, slot);
   };
-  int slot, page = fetch(slot);
+  int slot = -1, page = icur.unit < x1 ? fetch(slot) : -1;
   auto issue = [&](int t) {
     if (icur.unit < x1) {
       const int st = t % kStages;
@@ -312,6 +342,10 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
 
   uint32_t qa[8][4];
   float o[16][4];
+#pragma unroll
+  for (int nt = 0; nt < 16; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
   float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
   int seg_local = 0;                          // first chunk of this CTA's piece of the segment
   bool first_piece = true, fresh = true;
@@ -349,17 +383,17 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
       o[nt][2] = o[nt][2] * fb + y.x * gb; o[nt][3] = o[nt][3] * fb + y.y * gb;
     }
   };
-  auto finish = [&](bool whole) {
+  // Leaves the warps' partials in shared memory: `parts` of them, `part_rows`
+  // rows apart.
+  const int parts = p.rows <= 8 ? kWarps : 2, part_rows = p.rows <= 8 ? 8 : kGroup;
+  auto gather = [&]() {
     l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
     l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
     l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
     l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-    int parts, part_rows;
     if (p.rows <= 8) {
-      parts = kWarps; part_rows = 8;
       put(join + warp * 8 * kPart);
     } else {
-      parts = 2; part_rows = kGroup;
       if (warp >= 2) put(join + (warp - 2) * kGroup * kPart);
       __syncthreads();
       if (warp < 2) {
@@ -369,19 +403,29 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
       }
     }
     __syncthreads();
+  };
+  // Row r of them, joined.
+  auto joined = [&](int r, float& m, float& l) -> float4 {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    m = -INFINITY;
+    l = 0.f;
+    for (int w = 0; w < parts; ++w) m = fmaxf(m, join[(w * part_rows + r) * kPart]);
+    for (int w = 0; w < parts; ++w) {
+      const float* from = join + (w * part_rows + r) * kPart;
+      const float f = weight2(from[0], m);
+      const float4 y = *reinterpret_cast<const float4*>(from + 4 + lane * 4);
+      l += f * from[1];
+      x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
+    }
+    return x;
+  };
+  auto finish = [&](bool whole) {
+    gather();
     const int n = p.ag_n[cur.a], j0 = p.ag_start[cur.a];
     float* part = p.part + ((int64_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * p.rows * kPart;
     for (int r = warp; r < n; r += kWarps) {
-      float m = -INFINITY, l = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < parts; ++w) m = fmaxf(m, join[(w * part_rows + r) * kPart]);
-      for (int w = 0; w < parts; ++w) {
-        const float* from = join + (w * part_rows + r) * kPart;
-        const float f = weight2(from[0], m);
-        const float4 y = *reinterpret_cast<const float4*>(from + 4 + lane * 4);
-        l += f * from[1];
-        x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
-      }
+      float m, l;
+      const float4 x = joined(r, m, l);
       if (whole) {
         write_row<F16>(p, cur.b, j0 + r, m, l, x, lane);
       } else {
@@ -507,13 +551,61 @@ paged_decode_kernel(const __grid_constant__ DecodeParams p) {
     }
     __syncwarp();                             // stage st is free for chunk t + kStages
     const bool seg_end = cur.local + 1 == cur.nc;
-    if (seg_end || cur.unit + 1 == x1) {
+    if (p.ranks == 0 && (seg_end || cur.unit + 1 == x1)) {
       finish(seg_end && seg_local == 0);
       first_piece = false;
       fresh = true;
     }
   }
   cp_async_wait<0>();
+  if (p.ranks == 0) return;
+
+  // the cluster's CTAs hold a part of the segment each
+  const int seg = blockIdx.x / p.ranks, rank = blockIdx.x - seg * p.ranks;
+  const int b = seg / p.n_ag, a = seg - b * p.n_ag, n = p.ag_n[a], j0 = p.ag_start[a];
+  gather();
+  if (p.ranks == 1) {
+    for (int r = warp; r < n; r += kWarps) {
+      float m, l;
+      const float4 x = joined(r, m, l);
+      write_row<F16>(p, b, j0 + r, m, l, x, lane);
+    }
+    return;
+  }
+  for (int r = warp; r < n; r += kWarps) {    // this CTA's sums, in the place of the first partial
+    float m, l;
+    const float4 x = joined(r, m, l);
+    __syncwarp();
+    float* to = join + r * kPart;
+    if (lane == 0) { to[0] = m; to[1] = l; }
+    *reinterpret_cast<float4*>(to + 4 + lane * 4) = x;
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int r = rank + warp * p.ranks; r < n; r += p.ranks * kWarps) {
+    float ms[kMaxRanks], ls[kMaxRanks];
+    float4 os[kMaxRanks];
+#pragma unroll
+    for (int y = 0; y < kMaxRanks; ++y) {     // past the last rank, its again
+      const float* from = cluster.map_shared_rank(join, min(y, p.ranks - 1)) + r * kPart;
+      ms[y] = from[0];
+      ls[y] = from[1];
+      os[y] = *reinterpret_cast<const float4*>(from + 4 + lane * 4);
+    }
+    float m = -INFINITY, l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int y = 0; y < kMaxRanks; ++y) m = fmaxf(m, ms[y]);
+#pragma unroll
+    for (int y = 0; y < kMaxRanks; ++y) {
+      if (y >= p.ranks) break;
+      const float f = weight2(ms[y], m);
+      l += f * ls[y];
+      x.x += f * os[y].x; x.y += f * os[y].y; x.z += f * os[y].z; x.w += f * os[y].w;
+    }
+    write_row<F16>(p, b, j0 + r, m, l, x, lane);
+  }
+  cluster.sync();                             // no CTA leaves while its sums may be read
 }
 
 // Joins the partials of the segments that the runs cut: CTA (c, r) looks at
@@ -680,14 +772,42 @@ size_t paged_decode_ws_bytes(int B, int max_len, int n_heads, int window, int si
   return n;
 }
 
+// CTAs that share a segment, or 0 for runs over the whole list: where a
+// segment of the longest length is at most six chunks a CTA and all CTAs run at
+// once, the second kernel's launch and start (about 3 us) are more than what an
+// even cut saves.
+static int choose_ranks(int64_t segments, int64_t chunks) {
+  int ranks = 1;
+  while (ranks < kMaxRanks && chunks > ranks * 2 && segments * ranks * 2 <= kMaxCtas) ranks *= 2;
+  return segments * ranks <= kMaxCtas && chunks <= ranks * 6 ? ranks : 0;
+}
+
 template <bool F16>
 static cudaError_t launch_typed(const DecodeParams& p, int grid, cudaStream_t stream) {
   const size_t smem = sizeof(Smem);
   cudaError_t e =
       cudaFuncSetAttribute(paged_decode_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_decode_kernel<F16>, dim3(grid), dim3(kThreads), smem, stream, p);
-  if (e != cudaSuccess) return e;
+  if (p.ranks <= 1) {
+    e = launch_pdl(paged_decode_kernel<F16>, dim3(grid), dim3(kThreads), smem, stream, p);
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<F16>, p);
+  }
+  if (e != cudaSuccess || p.ranks > 0) return e;
   return launch_pdl(paged_join_kernel<F16>, dim3(grid, p.rows), dim3(kThreads), 0, stream, p);
 }
 
@@ -739,9 +859,11 @@ cudaError_t launch_paged_decode(const PagedView& c, const void* q, int64_t q_sb,
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  int64_t grid = (int64_t)B * p.n_ag * (p.att_cap / kChunk);
+  const int64_t segments = (int64_t)B * p.n_ag;
+  p.ranks = choose_ranks(segments, p.att_cap / kChunk);
+  int64_t grid = segments * (p.ranks > 0 ? p.ranks : p.att_cap / kChunk);
   const int most = sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
-  if (grid > most) grid = most;
+  if (p.ranks == 0 && grid > most) grid = most;
   e = f16 ? launch_typed<true>(p, (int)grid, stream) : launch_typed<false>(p, (int)grid, stream);
   if (e != cudaSuccess) return e;
   if (w_out) {

@@ -320,6 +320,9 @@ DECODE = [
     ([777, 3], 4, 4, 128, 1, 1, [1, 3]),
     ([2050, 0, 1, 129], 32, 4, 256, None, 0, list(range(32))),
     ([9000], 8, 1, 64, None, 0, list(range(8))),
+    ([6000, 0, 100], 16, 1, 64, None, 0, list(range(16))),
+    ([3000, 129, 0, 64], 24, 2, 32, None, 0, [0, 5, 11, 12, 13, 14, 15, 16, 17, 18, 19, 20, 21, 22]),
+    ([200] * 70, 8, 4, 16, None, 0, list(range(8))),
     ([70] * 150, 2, 2, 16, None, 0, [0, 1]),
     ([64] * 40 + [3000] + [0] * 130 + [5], 4, 4, 2, 1000, 3, [0, 1, 2, 3]),
 ]
