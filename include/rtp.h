@@ -588,7 +588,7 @@ typedef struct {
  *   heads    host int32 [n_heads], distinct.
  *   lse      fp32 [n_heads, T] device out, contiguous, or NULL; row j belongs
  *            to heads[j], rows of sequences written.
- *   T >= 0, S >= 1, Hq <= 256, window >= 1, scale > 0.
+ *   T >= 0, S >= 1, Hq <= 256, window >= 1, 0 < scale < 1e38.
  *   ws       rtp_workspace_size_attn_packed() bytes: the status word (see
  *            rtp_get_device_status).
  */
@@ -660,7 +660,7 @@ RTP_API rtp_status rtp_paged_append(const rtp_paged_cache* cache, const void* k,
  *   ws       rtp_workspace_size_paged_attn_decode(B, max_len, n_heads, window,
  *            sink, weights_out != NULL) bytes; the status word always reads
  *            RTP_OK (the kernels never wait on one another on the device).
- *   Hq / Hkv <= 16, Hq <= 256, 1 <= B <= 65535, window >= 1, sink >= 0, scale > 0.
+ *   Hq / Hkv <= 16, Hq <= 256, 1 <= B <= 65535, window >= 1, sink >= 0, 0 < scale < 1e38.
  */
 RTP_API size_t rtp_workspace_size_paged_attn_decode(int B, int max_len, int n_heads, int window, int sink,
                                                     int with_weights);

@@ -14,6 +14,9 @@ namespace {
 
 constexpr int64_t kMaxRows = 1 << 30;
 
+// A softmax scale that stays finite in the log2 domain.
+bool scale_ok(float s) { return s > 0.f && s < 1e38f; }
+
 bool dtype_ok(rtp_dtype d) { return d == RTP_BF16 || d == RTP_F16; }
 
 // Element strides of a dimension of n rows: a multiple of 8, and rows do not
@@ -69,7 +72,7 @@ rtp_status rtp_attn_packed(const void* q, rtp_strides qs, const void* k, rtp_str
                            const int32_t* heads, int n_heads, const int32_t* cu_seqlens, int S, int window,
                            float scale, float* lse, void* ws, size_t ws_bytes, rtp_stream_t stream) {
   if (T < 0 || S < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !cu_seqlens) return RTP_ERR_INVALID_ARG;
-  if (!dtype_ok(dtype) || window < 1 || !(scale > 0.f)) return RTP_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || window < 1 || !scale_ok(scale)) return RTP_ERR_INVALID_ARG;
   rtp_status st = check_heads(heads, n_heads, Hq);
   if (st != RTP_OK) return st;
   if (Hq > 256 || T > kMaxRows || S > kMaxRows) return RTP_ERR_UNSUPPORTED;
@@ -99,7 +102,7 @@ rtp_status rtp_attn_key_weights(const void* q, rtp_strides qs, const void* k, rt
                                 const float* lse, int n_obs, int window, float scale, float* weights, void* ws,
                                 size_t ws_bytes, rtp_stream_t stream) {
   if (T < 0 || S < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !cu_seqlens) return RTP_ERR_INVALID_ARG;
-  if (!dtype_ok(dtype) || window < 1 || n_obs < 1 || !(scale > 0.f)) return RTP_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || window < 1 || n_obs < 1 || !scale_ok(scale)) return RTP_ERR_INVALID_ARG;
   rtp_status st = check_heads(heads, n_heads, Hq);
   if (st != RTP_OK) return st;
   if (Hq > 256 || T > kMaxRows || S > kMaxRows) return RTP_ERR_UNSUPPORTED;
@@ -152,7 +155,7 @@ rtp_status rtp_paged_attn_decode(const void* q, rtp_strides qs, const rtp_paged_
   if (st != RTP_OK) return st;
   if (!q || !o || !lens || !dtype_ok(dtype)) return RTP_ERR_INVALID_ARG;
   if (B < 1 || Hq < 1 || Hq % view.Hkv != 0 || max_len < 1 || max_len > view.capacity) return RTP_ERR_INVALID_ARG;
-  if (window < 1 || sink < 0 || !(scale > 0.f)) return RTP_ERR_INVALID_ARG;
+  if (window < 1 || sink < 0 || !scale_ok(scale)) return RTP_ERR_INVALID_ARG;
   if (weights_out && !cache->weights) return RTP_ERR_INVALID_ARG;
   if ((st = check_heads(heads, n_heads, Hq)) != RTP_OK) return st;
   if (Hq > 256 || Hq / view.Hkv > 16 || B > 65535) return RTP_ERR_UNSUPPORTED;

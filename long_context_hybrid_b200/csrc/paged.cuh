@@ -66,7 +66,7 @@ __device__ __forceinline__ bool packed_tile(const int32_t* cu, int S, int T, int
   *n = b > a ? b - a : 0;
   const int64_t r = (number - ((a >> kShift) + (int64_t)i)) << kShift;
   *row0 = (int)r;
-  return r < *n;
+  return r >= 0 && r < *n;                     // offsets that decrease end up on either side
 }
 
 // 16-bit element types of the serving kernels.

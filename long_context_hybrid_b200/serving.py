@@ -112,11 +112,27 @@ class PagedCache:
     caller's; the pages they hold are written by ``paged_append`` and
     ``cache_evict``."""
 
-    __slots__ = ("k", "v", "table", "weights", "packed")
+    __slots__ = ("_tensors", "packed")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, weights: Optional[torch.Tensor] = None):
         self.packed = (_native or _marshal()).cache(k, v, table, weights)
-        self.k, self.v, self.table, self.weights = k, v, table, weights
+        self._tensors = (k, v, table, weights)     # what `packed` points to, for good
+
+    @property
+    def k(self) -> torch.Tensor:
+        return self._tensors[0]
+
+    @property
+    def v(self) -> torch.Tensor:
+        return self._tensors[1]
+
+    @property
+    def table(self) -> torch.Tensor:
+        return self._tensors[2]
+
+    @property
+    def weights(self) -> Optional[torch.Tensor]:
+        return self._tensors[3]
 
     @property
     def num_pages(self) -> int:

@@ -690,3 +690,39 @@ def test_long_cache_offsets_pass_32_bits():
     for h in range(2):
         ref, _, _, pv, size = SO.decode_head(f64(q)[0, h], f64(kk)[:, 0], f64(vv)[:, 0], np.arange(n), SCALE)
         check_o(f64(o)[0, h], ref, pv, size, torch.bfloat16, n, f"head {h}")
+
+
+@pytest.mark.parametrize("cu", [[0, 300, 100, 400], [500, -5, 10 ** 9, 20], [-10, -10, -10, -10], [400, 300, 200, 0],
+                                [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 17], [390, 390, 400, 1000]])
+def test_bad_offsets_stay_inside_the_tensors(cu):
+    """Offsets that decrease or leave [0, T]: nothing outside the tensors is
+    touched (guard rows around every output), and the calls end."""
+    T, guard, Hq, Hkv = 400, 64, 4, 2
+    gen = torch.Generator().manual_seed(12)
+    room = lambda H: rnd((T + 2 * guard, H, D), torch.bfloat16, gen).to(DEV)  # noqa: E731
+    inner = slice(guard, guard + T)
+    q, k, v = room(Hq)[inner], room(Hkv)[inner], room(Hkv)[inner]
+    o_room = torch.full((T + 2 * guard, Hq, D), SENTINEL, dtype=torch.bfloat16, device=DEV)
+    lse_room = torch.full((Hq * T + 2 * guard,), SENTINEL, device=DEV)
+    w_room = torch.full((Hkv * T + 2 * guard,), SENTINEL, device=DEV)
+    lse, w = lse_room[guard:-guard].view(Hq, T), w_room[guard:-guard].view(Hkv, T)
+    cu_d = torch.tensor(cu, dtype=torch.int64).to(torch.int32).to(DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    rtp.attn_packed(q, k, v, o_room[inner], [0, 1, 2, 3], cu_d, lse=lse, ws=ws)
+    assert rtp.workspace_status(ws) == 0
+    for n_obs in (None, 20):
+        rtp.attn_key_weights(q, k, lse, w, [0, 1, 2, 3], cu_d, n_obs=n_obs, ws=ws)
+        assert rtp.workspace_status(ws) == 0
+    cache, _ = make_cache([T] * 3, Hkv, 16, torch.bfloat16, 13)
+    rtp.paged_append(cache, k, v, cu_d, torch.tensor([0, 2 ** 31 - 1, -2 ** 31], dtype=torch.int64).to(torch.int32)
+                     .to(DEV))
+    torch.cuda.synchronize()
+    for x in (o_room[:guard], o_room[-guard:], lse_room[:guard], lse_room[-guard:], w_room[:guard], w_room[-guard:]):
+        assert (x == SENTINEL).all()
+
+
+def test_cache_is_bound_to_its_tensors():
+    cache, _ = make_cache([5], 1, 16, torch.bfloat16, 14)
+    for name in ("k", "v", "table", "weights"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, None)
