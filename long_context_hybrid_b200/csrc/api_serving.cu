@@ -76,7 +76,7 @@ rtp_status rtp_attn_packed(const void* q, rtp_strides qs, const void* k, rtp_str
   rtp_status st = check_heads(heads, n_heads, Hq);
   if (st != RTP_OK) return st;
   if (Hq > 256 || T > kMaxRows || S > kMaxRows) return RTP_ERR_UNSUPPORTED;
-  if (((int64_t)T / 256 + S) * n_heads > INT32_MAX) return RTP_ERR_UNSUPPORTED;
+  if (((int64_t)T / 128 + S) * n_heads > INT32_MAX) return RTP_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < kStatusBytes || !aligned256(ws)) return RTP_ERR_WORKSPACE;
   if (T > 0) {
     if (!q || !k || !v || !o) return RTP_ERR_INVALID_ARG;

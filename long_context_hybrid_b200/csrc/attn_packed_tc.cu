@@ -5,13 +5,14 @@
 //   o[t] = sum_u p_u v_u,  p_u = exp(scale q[t].k[u] - lse[t]),
 //   u in t's sequence, u <= t, t - u < window.
 //
-// A CTA computes 256 consecutive query rows of one sequence and head against
+// A CTA computes 256 consecutive query rows of one sequence and head, or 128
+// where the prompts are short (Cfg below), against
 // tiles of 128 keys aligned to the sequence's start. The lengths stay on the
 // device: the grid covers every tile number that any lengths could need, and
 // a CTA finds its sequence by a search of the offsets; numbers run downwards, so that
 // within a sequence the rows with most keys start first.
 //
-// Warp roles (384 threads):
+// Warp roles (384 threads; of 256 with one query tile):
 //   warp 0     TMA producer: two Q tiles, then K and V tiles (32 KB each,
 //              128-byte swizzle) through a ring of five: a stage holds either, so
 //              the ring is two and a half key tiles deep beside 64 KB of Q;
@@ -43,13 +44,26 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kTileRows = 256;                       // query rows of a CTA
 constexpr int kKeyTile = 128;
-constexpr int kRing = 5;
 constexpr uint32_t kStage = 32768;                   // one K or V tile: [D half][128 rows][128 B]
-constexpr uint32_t kRingOff = 2 * kStage;            // behind the two Q tiles
-constexpr uint32_t kTmemCols = 512;                  // tile t: S at 256 t, O at 256 t + 128
+// A CTA of NQ query tiles. Two: one CTA an SM, each key tile read once for both.
+// One, with a ring of one key tile: two CTAs an SM, so that one computes while
+// the other begins or ends, which is most of the time of short prompts. Measured,
+// us with two tiles and with one: 48 prompts of 16 tokens, 8 heads 21.6, 15.5;
+// 32 heads 73, 47; 64 x 128 tokens 118, 81; 64 x 200 179, 160; 32 x 256 95, 86;
+// 16 x 500 104, 97; 8 x 1000 125, 123; a prompt of 4000 among 60 of 20 234, 198.
+template <int NQ>
+struct Cfg {
+  static constexpr int kThreads = 128 + 128 * NQ;
+  static constexpr int kTileRows = 128 * NQ;         // query rows of a CTA
+  static constexpr int kRing = NQ == 2 ? 5 : 2;
+  static constexpr uint32_t kRingOff = NQ * kStage;  // behind the Q tiles
+  static constexpr uint32_t kTmemCols = 256 * NQ;    // tile t: S at 256 t, O at 256 t + 128
+  // a stage of an odd ring holds K and V in turn
+  static constexpr int phase(int turn) { return (kRing & 1 ? turn >> 1 : turn) & 1; }
+};
+constexpr int kShortPrompt = 512;                    // tokens of a prompt, on average
+constexpr int kSMs = 148;
 constexpr int kStatusTimeout = 4;
 // Few units: the CTAs of a cluster split the key tiles of one. At the end each
 // query tile's partials (64 KB and a maximum and sum a row) go to the CTA whose
@@ -66,20 +80,24 @@ struct PackedParams {
   float* lse;                                        // [n_heads, T] or NULL
   int S, T, G, window, n_heads;
   int ranks;                                         // CTAs that share a unit's keys (a cluster): 1 to kMaxRanks
-  int64_t n_numbers;                                 // tile numbers: floor(T / 256) + S
+  int64_t n_numbers;                                 // tile numbers: floor(T / rows of a CTA) + S
   float scale_log2;
   uint8_t head[kMaxHeads];
 };
 
+constexpr int kMaxRing = 5;
 struct Bars {
-  uint64_t q_full[2], full[kRing], empty[kRing], v_ok[kRing];
+  // K and V have a barrier each at every stage: the guard waits for V alone,
+  // and could not tell a stage's phases apart if K's were among them
+  uint64_t q_full[2], full[2][kMaxRing], empty[kMaxRing], v_ok[kMaxRing];
   uint64_t s_full[2], p_full[2][2], o_full[2], fin;  // p_full[query tile][64-key half]
   uint32_t tmem_base;
   int abort;
   int poison;                                        // the guard met a non-finite value of the sequence
 };
 
-constexpr size_t kSmemBytes = 1024 + kRingOff + kRing * kStage + sizeof(Bars);
+template <int NQ>
+constexpr size_t kSmemBytes = 1024 + Cfg<NQ>::kRingOff + Cfg<NQ>::kRing * kStage + sizeof(Bars);
 
 // Halves of a pair whose exponent is all ones, as bits 15 and 31.
 template <bool F16>
@@ -89,10 +107,13 @@ __device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
 
 }  // namespace
 
-template <bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool F16, int NQ>
+__global__ void __launch_bounds__(Cfg<NQ>::kThreads, NQ == 2 ? 1 : 2)
 attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, int* status) {
+  using C = Cfg<NQ>;
+  constexpr int kRing = C::kRing, kTileRows = C::kTileRows;
+  constexpr uint32_t kRingOff = C::kRingOff;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -100,7 +121,7 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
   Bars& bars = *reinterpret_cast<Bars*>(smem + kRingOff + kRing * kStage);
   volatile int* abort_flag = &bars.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ranks = p.ranks, rank = blockIdx.x % ranks, unit = blockIdx.x / ranks;
+  const int ranks = NQ == 2 ? p.ranks : 1, rank = blockIdx.x % ranks, unit = blockIdx.x / ranks;
   const int jh = unit % p.n_heads;
   const int h = p.head[jh], g = h / p.G;
   int c0, n, row0;                                   // the sequence's first row and length, the CTA's first row in it
@@ -111,22 +132,22 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
   // key tiles kt_lo .. kt_lo + n_tiles - 1 (of 128 keys); query tile t takes
   // those of [first[t], last[t]), counted from kt_lo
   const int window = p.window;
-  int first[2], last[2];
+  int first[NQ], last[NQ];
   const int kt_all = max(0, row0 - window + 1) / kKeyTile;
   int kt_lo = kt_all;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < NQ; ++t) {
     const int r = row0 + t * 128;
     const bool any = r < n;
     first[t] = any ? max(0, r - window + 1) / kKeyTile - kt_lo : 0;
     last[t] = any ? min(n - 1, r + 127) / kKeyTile + 1 - kt_lo : 0;
   }
-  const int n_all = max(last[0], last[1]);
+  const int n_all = max(last[0], last[NQ - 1]);
   int n_tiles = n_all;
   if (ranks > 1) {                                   // this rank's part of them
     const int lo = rank * n_all / ranks, hi = (rank + 1) * n_all / ranks;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < NQ; ++t) {
       first[t] = min(max(first[t], lo), hi) - lo;
       last[t] = max(min(max(last[t], lo), hi) - lo, first[t]);
     }
@@ -148,7 +169,7 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
   };
   auto load_kv = [&](int r) {                          // item 2j is K of tile j, 2j + 1 its V
     const int s = r % kRing;
-    const uint32_t dst = sb + kRingOff + s * kStage, bar = smem_u32(&bars.full[s]);
+    const uint32_t dst = sb + kRingOff + s * kStage, bar = smem_u32(&bars.full[r & 1][s]);
     const CUtensorMap* map = (r & 1) ? &tmV : &tmK;
     const int key = c0 + (kt_lo + (r >> 1)) * kKeyTile;
     mbar_arrive_expect_tx(bar, kStage);
@@ -156,14 +177,15 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     tma_load_4d(dst + 16384, map, bar, 64, g, key, 0);
   };
   if (tid == 0) {
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < NQ; ++t) {
       mbar_init(smem_u32(&bars.q_full[t]), 1);
       mbar_init(smem_u32(&bars.s_full[t]), 1);
       mbar_init(smem_u32(&bars.o_full[t]), 1);
       for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&bars.p_full[t][x]), 4);
     }
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(smem_u32(&bars.full[s]), 1);
+      mbar_init(smem_u32(&bars.full[0][s]), 1);
+      mbar_init(smem_u32(&bars.full[1][s]), 1);
       mbar_init(smem_u32(&bars.empty[s]), 1);
       mbar_init(smem_u32(&bars.v_ok[s]), 2);
     }
@@ -175,21 +197,23 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     if (last[0] > first[0]) load_q(0);
     for (int r = 0; r < min(kRing, 2 * n_tiles); ++r) {
       load_kv(r);
-      if (r == 0 && last[1] > first[1]) load_q(1);
+      if (NQ == 2 && r == 0 && last[NQ - 1] > first[NQ - 1]) load_q(1);
     }
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&bars.tmem_base), kTmemCols);
+    tmem_alloc(smem_u32(&bars.tmem_base), C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  constexpr uint32_t tmem = 0;                       // every column is allocated, so the address is 0
-  // 128 * (80 + 2 * 208) registers of the launch's 384 * 168: a softmax thread
-  // holds its row of 128 scores
+  // with every column allocated the address is 0, known without a load
+  const uint32_t tmem = NQ == 2 ? 0u : bars.tmem_base;
+  // A softmax thread holds its row of 128 scores: 128 * (80 + 2 * 208) registers
+  // of the launch's 384 * 168, or 128 * (56 + 200) of its 256 * 128.
   if (warp < 4) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+   if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+   else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
    if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -207,10 +231,10 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
         }
       }
       if (*abort_flag) {
-        if (last[0] > first[0]) wait_short(smem_u32(&bars.q_full[0]), 0);
-        if (last[1] > first[1]) wait_short(smem_u32(&bars.q_full[1]), 0);
+        for (int t = 0; t < NQ; ++t)
+          if (last[t] > first[t]) wait_short(smem_u32(&bars.q_full[t]), 0);
         for (int r = max(0, issued - kRing); r < issued; ++r)
-          wait_short(smem_u32(&bars.full[r % kRing]), (r / kRing) & 1);
+          wait_short(smem_u32(&bars.full[r & 1][r % kRing]), C::phase(r / kRing));
       }
     }
    } else if (warp == 1) {
@@ -220,39 +244,41 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
                    v_desc = desc_mn_major(sb + kRingOff);
     // each tile's first scores (the second's first key tile may be number 1)
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < NQ; ++t) {
       if (last[t] > first[t]) {
         mbar_pass(smem_u32(&bars.q_full[t]), 0, abort_flag);
-        mbar_pass(smem_u32(&bars.full[2 * first[t]]), 0, abort_flag);
+        mbar_pass(smem_u32(&bars.full[0][2 * first[t]]), 0, abort_flag);
         tc_fence_after();
-        issue_qk<F16>(on, t * 256u, q_desc + t * (kStage >> 4), k_desc + (uint64_t)(2 * first[t]) * (kStage >> 4));
+        issue_qk<F16>(on, tmem + t * 256u, q_desc + t * (kStage >> 4), k_desc + (uint64_t)(2 * first[t]) * (kStage >> 4));
         commit_if(on, smem_u32(&bars.s_full[t]));
       }
     }
     if (n_tiles > 0) commit_if(on, smem_u32(&bars.empty[0]));
     // stage and turn of the K item of tile j + 1 and of the V item of tile j
-    int k_st = 2, k_turn = 0, v_st = 1, v_turn = 0;
+    int k_st = 2 % kRing, k_turn = 2 / kRing, v_st = 1, v_turn = 0;
     for (int j = 0; j < n_tiles; ++j) {
       const uint64_t v_d = v_desc + (uint64_t)v_st * (kStage >> 4);
       const uint64_t k_d = k_desc + (uint64_t)k_st * (kStage >> 4);
       // v_ok of every tile, so that the guard never falls a ring behind
-      mbar_pass(smem_u32(&bars.full[v_st]), v_turn & 1, abort_flag);
-      mbar_pass(smem_u32(&bars.v_ok[v_st]), (v_turn >> 1) & 1, abort_flag);
-      if (j + 1 < n_tiles) mbar_pass(smem_u32(&bars.full[k_st]), k_turn & 1, abort_flag);
+      mbar_pass(smem_u32(&bars.full[1][v_st]), C::phase(v_turn), abort_flag);
+      mbar_pass(smem_u32(&bars.v_ok[v_st]), C::phase(v_turn), abort_flag);
+      if (NQ == 2 && j + 1 < n_tiles) mbar_pass(smem_u32(&bars.full[0][k_st]), C::phase(k_turn), abort_flag);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < NQ; ++t) {
         if (j >= first[t] && j < last[t]) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             mbar_pass(smem_u32(&bars.p_full[t][half]), (j - first[t]) & 1, abort_flag);
             tc_fence_after();
-            issue_pv<F16>(on, t * 256u + 128u, t * 256u + half * 32u, v_d, half, half || j > first[t]);
+            issue_pv<F16>(on, tmem + t * 256u + 128u, tmem + t * 256u + half * 32u, v_d, half, half || j > first[t]);
           }
           if (j + 1 == last[t]) commit_if(on, smem_u32(&bars.o_full[t]));
         }
         if (j + 1 > first[t] && j + 1 < last[t]) {
+          // a ring of one key tile: K of the next one follows this one's scores
+          if (NQ == 1) mbar_pass(smem_u32(&bars.full[0][k_st]), C::phase(k_turn), abort_flag);
           tc_fence_after();
-          issue_qk<F16>(on, t * 256u, q_desc + t * (kStage >> 4), k_d);
+          issue_qk<F16>(on, tmem + t * 256u, q_desc + t * (kStage >> 4), k_d);
           commit_if(on, smem_u32(&bars.s_full[t]));
         }
       }
@@ -269,13 +295,10 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
    } else {
     // ------------------------------------------------------------ V guard
     const int gt = tid - 64;
-    for (int r = 0; r < 2 * n_tiles; ++r) {
-      // K items are waited for too: copies may complete out of order, and a
-      // wait that skips a turn of a stage could not tell it from the last one
-      const int s = r % kRing, j = r >> 1;
-      const bool w = mbar_spin(smem_u32(&bars.full[s]), (r / kRing) & 1, abort_flag);
+    for (int j = 0; j < n_tiles; ++j) {
+      const int r = 2 * j + 1, s = r % kRing;
+      const bool w = mbar_spin(smem_u32(&bars.full[1][s]), C::phase(r / kRing), abort_flag);
       if (!__all_sync(0xffffffffu, w)) break;
-      if (!(r & 1)) continue;
       if (masked(kt_lo + j)) {
         uint4* tile = reinterpret_cast<uint4*>(smem + kRingOff + s * kStage);
         const int there = n - (kt_lo + j) * kKeyTile;     // rows of the tile that are keys of the sequence
@@ -304,9 +327,10 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     cluster_meet();
    }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ------------------------------------------------------------ softmax
-    const int t = (warp - 4) >> 2;                  // query tile of this warpgroup
+    const int t = NQ == 2 ? (warp - 4) >> 2 : 0;    // query tile of this warpgroup
     const int r = (warp & 3) * 32 + lane;           // row within the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int i = row0 + t * 128 + r;               // row within the sequence
@@ -501,7 +525,7 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
     volatile int* poison = &bars.poison;
     if (ranks == 1) {
       if (here && ok) write_out(std::false_type{}, *poison != 0);
-    } else {
+    } else if constexpr (NQ == 2) {
       cluster_meet();                                // nobody's query tiles and ring are in use any more
       const bool whole = ok || !here;
       if (rank != t && whole && row0 + t * 128 < n) {
@@ -532,21 +556,21 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
   if (tid == 0 && bars.abort) atomicExch(status, kStatusTimeout);
 }
 
-template <bool F16>
+template <bool F16, int NQ>
 static cudaError_t launch_typed(const PackedParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, int* status, cudaStream_t stream) {
-  cudaError_t e =
-      cudaFuncSetAttribute(attn_packed_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  auto kernel = attn_packed_kernel<F16, NQ>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<NQ>);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.n_numbers * p.n_heads * p.ranks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.blockDim = dim3(Cfg<NQ>::kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes<NQ>;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -555,7 +579,7 @@ static cudaError_t launch_typed(const PackedParams& p, const CUtensorMap& tq, co
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.ranks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_packed_kernel<F16>, p, tq, tk, tv, status);
+  return cudaLaunchKernelEx(&cfg, kernel, p, tq, tk, tv, status);
 }
 
 // How many CTAs share a unit's keys, from what the host knows: the units and
@@ -568,13 +592,13 @@ static cudaError_t launch_typed(const PackedParams& p, const CUtensorMap& tq, co
 // heads 38, 38; 1024, 32 heads 24, 32; 100 tokens, 8 heads 8, 11.
 static int choose_ranks(int64_t units, int mean_len, int window) {
   const bool cut = window < mean_len;
-  const double longest = ((cut ? (double)window + kTileRows : mean_len) + kKeyTile - 1) / kKeyTile;
-  const double work = units * (cut ? longest : (longest + 1) / 2) / 148.0;
+  const double longest = ((cut ? (double)window + Cfg<2>::kTileRows : mean_len) + kKeyTile - 1) / kKeyTile;
+  const double work = (double)units * (cut ? longest : (longest + 1) / 2) / kSMs;
   int best = 1;
   double least = 0;
   for (int r = 1; r <= kMaxRanks; ++r) {
-    if (r > 2 && units * r > 148) break;
-    const double alone = longest / r + (r > 1 ? 2 : 0), share = work + units * r * (r > 1 ? 4 : 2) / 148.0;
+    if (r > 2 && units * r > kSMs) break;
+    const double alone = longest / r + (r > 1 ? 2 : 0), share = work + (double)units * r * (r > 1 ? 4 : 2) / kSMs;
     const double time = alone > share ? alone : share;
     if (r == 1 || time < 0.9 * least) {
       best = r;
@@ -598,11 +622,20 @@ cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4
   p.v = v.p; p.v_sn = v.sn; p.v_sh = v.sh;
   p.cu = cu; p.lse = lse;
   p.S = S; p.T = T; p.G = Hq / Hkv; p.window = window; p.n_heads = n_heads;
-  p.n_numbers = (int64_t)T / kTileRows + S;
-  p.ranks = choose_ranks(p.n_numbers * n_heads, T / S, window);
+  // Short prompts: one query tile a CTA, unless the SMs have room for all units
+  // at two (16 prompts of 100 tokens, 8 heads, 176 units: 9.4 us with two, 10.9
+  // with one), where a cluster may split them as well.
+  p.n_numbers = (int64_t)T / Cfg<2>::kTileRows + S;
+  const bool small = T / S <= kShortPrompt && p.n_numbers * n_heads > kSMs;
+  if (small) p.n_numbers = (int64_t)T / Cfg<1>::kTileRows + S;
+  p.ranks = small ? 1 : choose_ranks(p.n_numbers * n_heads, T / S, window);
   p.scale_log2 = scale * 1.4426950408889634f;
   for (int j = 0; j < n_heads; ++j) p.head[j] = (uint8_t)heads[j];
-  return f16 ? launch_typed<true>(p, tq, tk, tv, status, stream) : launch_typed<false>(p, tq, tk, tv, status, stream);
+  if (small)
+    return f16 ? launch_typed<true, 1>(p, tq, tk, tv, status, stream)
+               : launch_typed<false, 1>(p, tq, tk, tv, status, stream);
+  return f16 ? launch_typed<true, 2>(p, tq, tk, tv, status, stream)
+             : launch_typed<false, 2>(p, tq, tk, tv, status, stream);
 }
 
 }  // namespace rtp

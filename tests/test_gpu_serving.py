@@ -109,6 +109,13 @@ PACKED = [
     ([700, 65, 0, 300, 1, 129], 32, 4, 100, list(range(32)), 1, 0, 0),
     ([600, 300, 500], 8, 2, None, list(range(8)), 0, 0, 8),
     ([600, 300, 500], 8, 2, 129, list(range(8)), 0, 0, 0),
+    # short prompts and many tiles: one query tile a CTA; long ones: two
+    ([1, 513, 0, 128, 2, 127, 256, 129, 16, 1], 32, 8, None, list(range(1, 32, 2)), 2, 200, 8),
+    ([1, 513, 0, 128, 2, 127, 256, 129, 16, 1], 32, 8, 70, list(range(32)), 0, 0, 0),
+    ([9] * 90, 4, 1, None, [0, 3], 0, 1, 0),
+    ([1900, 5], 8, 1, 300, list(range(8)), 0, 0, 0),
+    ([1200, 1300], 20, 4, None, list(range(20)), 5, 0, 0),
+    ([1200, 1300], 20, 4, 150, list(range(20)), 0, 0, 0),
 ]
 
 
@@ -141,7 +148,7 @@ def test_attn_packed(case, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("window", [None, 40, 200])
-@pytest.mark.parametrize("Hq", [4, 12, 32])       # three CTAs, two, and one to a tile's keys
+@pytest.mark.parametrize("Hq", [4, 12, 32])       # three CTAs and two to a tile's keys; one, of one query tile
 def test_attn_packed_unattended_values_do_not_matter(dtype, window, Hq):
     """NaN and infinities in keys and values reach exactly the rows that attend
     them: not the neighbour sequence, not earlier rows, not rows whose window
