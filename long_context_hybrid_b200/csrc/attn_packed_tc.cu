@@ -51,7 +51,9 @@ constexpr uint32_t kStage = 32768;                   // one K or V tile: [D half
 // the other begins or ends, which is most of the time of short prompts. Measured,
 // us with two tiles and with one: 48 prompts of 16 tokens, 8 heads 21.6, 15.5;
 // 32 heads 73, 47; 64 x 128 tokens 118, 81; 64 x 200 179, 160; 32 x 256 95, 86;
-// 16 x 500 104, 97; 8 x 1000 125, 123; a prompt of 4000 among 60 of 20 234, 198.
+// 16 x 500 104, 97; 8 x 1000 125, 123; a prompt of 4000 among 60 of 20 234, 198;
+// windows over 32768 tokens, 8 heads: 64 keys 108, 99; 256 123, 115; 512 149, 144;
+// 1024 197, 201; over 4096 tokens, 4 heads: 64 16, 12; 512 21, 17; 1024 23, 25.
 template <int NQ>
 struct Cfg {
   static constexpr int kThreads = 128 + 128 * NQ;
@@ -62,7 +64,7 @@ struct Cfg {
   // a stage of an odd ring holds K and V in turn
   static constexpr int phase(int turn) { return (kRing & 1 ? turn >> 1 : turn) & 1; }
 };
-constexpr int kShortPrompt = 512;                    // tokens of a prompt, on average
+constexpr int kFewKeys = 512;                        // of a row: its window, or the prompts' mean length
 constexpr int kSMs = 148;
 constexpr int kStatusTimeout = 4;
 // Few units: the CTAs of a cluster split the key tiles of one. At the end each
@@ -622,11 +624,11 @@ cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4
   p.v = v.p; p.v_sn = v.sn; p.v_sh = v.sh;
   p.cu = cu; p.lse = lse;
   p.S = S; p.T = T; p.G = Hq / Hkv; p.window = window; p.n_heads = n_heads;
-  // Short prompts: one query tile a CTA, unless the SMs have room for all units
-  // at two (16 prompts of 100 tokens, 8 heads, 176 units: 9.4 us with two, 10.9
-  // with one), where a cluster may split them as well.
+  // Few keys a row: one query tile a CTA. For short prompts only where the SMs
+  // have no room for all units at two (4 prompts of 300 tokens, 8 heads: 12 us with
+  // either), as a cluster may split those.
   p.n_numbers = (int64_t)T / Cfg<2>::kTileRows + S;
-  const bool small = T / S <= kShortPrompt && p.n_numbers * n_heads > kSMs;
+  const bool small = T / S <= window ? T / S <= kFewKeys && p.n_numbers * n_heads > kSMs : window <= kFewKeys;
   if (small) p.n_numbers = (int64_t)T / Cfg<1>::kTileRows + S;
   p.ranks = small ? 1 : choose_ranks(p.n_numbers * n_heads, T / S, window);
   p.scale_log2 = scale * 1.4426950408889634f;

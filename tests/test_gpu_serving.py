@@ -114,8 +114,9 @@ PACKED = [
     ([1, 513, 0, 128, 2, 127, 256, 129, 16, 1], 32, 8, 70, list(range(32)), 0, 0, 0),
     ([9] * 90, 4, 1, None, [0, 3], 0, 1, 0),
     ([1900, 5], 8, 1, 300, list(range(8)), 0, 0, 0),
+    ([1900, 5], 8, 1, 600, list(range(8)), 0, 0, 0),
     ([1200, 1300], 20, 4, None, list(range(20)), 5, 0, 0),
-    ([1200, 1300], 20, 4, 150, list(range(20)), 0, 0, 0),
+    ([1200, 1300], 20, 4, 550, list(range(20)), 0, 0, 0),
 ]
 
 
@@ -147,13 +148,14 @@ def test_attn_packed(case, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("window", [None, 40, 200])
+@pytest.mark.parametrize("window", [None, 40, 200, 600])
 @pytest.mark.parametrize("Hq", [4, 12, 32])       # three CTAs and two to a tile's keys; one, of one query tile
 def test_attn_packed_unattended_values_do_not_matter(dtype, window, Hq):
     """NaN and infinities in keys and values reach exactly the rows that attend
     them: not the neighbour sequence, not earlier rows, not rows whose window
     has passed."""
-    lens = [150, 300, 90]
+    lens = [150, 1300 if window == 600 else 300, 90]
+    end = 150 + lens[1]
     (q, k, v), cu, cu_d = make_packed(lens, Hq, 2, dtype, 5)
     heads = list(range(Hq))
     G = Hq // 2
@@ -164,14 +166,14 @@ def test_attn_packed_unattended_values_do_not_matter(dtype, window, Hq):
         return o.float().cpu()
 
     clean = run()
-    at = {150 + 140: float("nan"), 150 + 299: float("inf"), 150 + 3: float("-inf")}   # all in sequence 1
+    at = {150 + 140: float("nan"), end - 1: float("inf"), 150 + 3: float("-inf")}   # all in sequence 1
     for row, bad in at.items():
         v[row, 0, 17] = bad
     k[150 + 250, 1] = float("nan")
     got = run()
     T = q.shape[0]
     t = torch.arange(T)[:, None]
-    reach = lambda row: ((t >= row) & (t < (min(450, row + window) if window else 450))).squeeze(1)  # noqa: E731
+    reach = lambda row: ((t >= row) & (t < (min(end, row + window) if window else end))).squeeze(1)  # noqa: E731
     hit_v = torch.zeros(T, dtype=torch.bool)
     for row in at:
         hit_v |= reach(row)
@@ -181,7 +183,7 @@ def test_attn_packed_unattended_values_do_not_matter(dtype, window, Hq):
     fine[reach(400), G:] = False
     assert torch.equal(fin, fine)
     assert torch.equal(got[fin], clean[fin])
-    only_inf = reach(449) & ~reach(290) & ~reach(153)
+    only_inf = reach(end - 1) & ~reach(290) & ~reach(153)
     assert (got[only_inf][:, :G, 17] == float("inf")).all()
 
 
