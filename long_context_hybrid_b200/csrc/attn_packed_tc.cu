@@ -101,6 +101,9 @@ struct Bars {
 template <int NQ>
 constexpr size_t kSmemBytes = 1024 + Cfg<NQ>::kRingOff + Cfg<NQ>::kRing * kStage + sizeof(Bars);
 
+// The n lowest bits, of any n.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 // Halves of a pair whose exponent is all ones, as bits 15 and 31.
 template <bool F16>
 __device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
@@ -362,8 +365,13 @@ attn_packed_kernel(const __grid_constant__ PackedParams p, const __grid_constant
           if (half) tc_wait_ld();
           if (kCut) {
 #pragma unroll
-            for (int c = half * 64; c < half * 64 + 64; ++c)
-              if (key0 + c > i || key0 + c <= i - window) v[c] = __float_as_uint(-INFINITY);
+            for (int x = half * 2; x < half * 2 + 2; ++x) {
+              // the keys of these 32 that the row attends, as bits
+              const uint32_t in = low_bits(i + 1 - key0 - x * 32) & ~low_bits(i - window + 1 - key0 - x * 32);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(in >> c & 1u)) v[x * 32 + c] = __float_as_uint(-INFINITY);
+            }
           }
 #pragma unroll
           for (int c = half * 64; c < half * 64 + 64; c += 2)
@@ -623,7 +631,7 @@ cudaError_t launch_attn_packed(const Tensor4& q, const Tensor4& k, const Tensor4
   p.o = o; p.o_sn = o_sn; p.o_sh = o_sh;
   p.v = v.p; p.v_sn = v.sn; p.v_sh = v.sh;
   p.cu = cu; p.lse = lse;
-  p.S = S; p.T = T; p.G = Hq / Hkv; p.window = window; p.n_heads = n_heads;
+  p.S = S; p.T = T; p.G = Hq / Hkv; p.window = min(window, T); p.n_heads = n_heads;
   // Few keys a row: one query tile a CTA. For short prompts only where the SMs
   // have no room for all units at two (4 prompts of 300 tokens, 8 heads: 12 us with
   // either), as a cluster may split those.
