@@ -117,11 +117,16 @@ PACKED = [
     ([1900, 5], 8, 1, 600, list(range(8)), 0, 0, 0),
     ([1200, 1300], 20, 4, None, list(range(20)), 5, 0, 0),
     ([1200, 1300], 20, 4, 550, list(range(20)), 0, 0, 0),
+    # several units a CTA, of one query tile and of two
+    ([70, 3, 200, 0, 129, 40] * 40, 16, 4, None, list(range(16)), 0, 0, 0),
+    ([70, 3, 200, 0, 129, 40] * 40, 16, 4, 50, list(range(16)), 1, 1, 0),
+    ([700, 1300, 2, 900], 32, 4, None, list(range(32)), 0, 0, 0),
+    ([700, 1300, 2, 900], 32, 4, 600, list(range(32)), 0, 4, 0),
 ]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("case", PACKED, ids=lambda c: f"{c[0]}w{c[3]}")
+@pytest.mark.parametrize("case", PACKED, ids=lambda c: f"{c[0][:12]}w{c[3]}")
 def test_attn_packed(case, dtype):
     lens, Hq, Hkv, window, heads, lead, tail, pad = case
     (q, k, v), cu, cu_d = make_packed(lens, Hq, Hkv, dtype, 11 + sum(lens), lead, tail, pad)
@@ -149,7 +154,7 @@ def test_attn_packed(case, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("window", [None, 40, 200, 600])
-@pytest.mark.parametrize("Hq", [4, 12, 32])       # three CTAs and two to a tile's keys; one, of one query tile
+@pytest.mark.parametrize("Hq", [4, 12, 32, 64])
 def test_attn_packed_unattended_values_do_not_matter(dtype, window, Hq):
     """NaN and infinities in keys and values reach exactly the rows that attend
     them: not the neighbour sequence, not earlier rows, not rows whose window
@@ -185,6 +190,26 @@ def test_attn_packed_unattended_values_do_not_matter(dtype, window, Hq):
     assert torch.equal(got[fin], clean[fin])
     only_inf = reach(end - 1) & ~reach(290) & ~reach(153)
     assert (got[only_inf][:, :G, 17] == float("inf")).all()
+
+
+def test_attn_packed_many_empty_prompts():
+    """Far more tile numbers than tiles: nothing runs out, and what is there is right."""
+    lens = [0] * 50000 + [5] + [0] * 40000 + [300, 0, 1] + [0] * 30000
+    Hq, Hkv = 8, 2
+    (q, k, v), cu, cu_d = make_packed(lens, Hq, Hkv, torch.bfloat16, 77)
+    o = torch.full_like(q, SENTINEL)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    rtp.attn_packed(q, k, v, o, list(range(Hq)), cu_d, ws=ws)
+    assert rtp.workspace_status(ws) == 0
+    og, qn, kn, vn = f64(o), f64(q), f64(k), f64(v)
+    for i, n in enumerate(lens):
+        if n == 0:
+            continue
+        rows = slice(cu[i], cu[i + 1])
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            ref, _, pv, size = SO.packed_head(qn[rows, h], kn[rows, g], vn[rows, g], n, SCALE)
+            check_o(og[rows, h], ref, pv, size, torch.bfloat16, n, f"sequence {i} head {h}")
 
 
 def test_attn_packed_long_prompt_sampled_rows():
