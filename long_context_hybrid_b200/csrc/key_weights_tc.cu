@@ -18,7 +18,7 @@
 //     CTA keeps the queries of a (sequence, KV head) in shared memory and
 //     streams key tiles past them, one unit of 128 keys after another; the
 //     warpgroups share every tile by columns. The last 64 rows of 4 prompts
-//     (40462 tokens, 8 heads a KV head): 48 us, and 119 us by the other kernel,
+//     (40462 tokens, 8 heads a KV head): 46 us, and 119 us by the other kernel,
 //     which reads the queries again for every 128 keys;
 //   * many: a CTA owns 128 keys and streams the query tiles of every head of
 //     the group past them. A cluster of 1 to 8 CTAs shares one set of keys when
@@ -29,7 +29,8 @@
 // Warp roles of both (640 threads): warp 0 TMA producer, warp 1 TMEM owner and
 // MMA issuer, and four warpgroups that sum, with a 128-column score buffer
 // each. (Every row of 6 prompts, 24657 tokens, 32 heads: 930 us with two
-// warpgroups of two buffers each, 694 us with four.)
+// warpgroups of two buffers each, 695 us with four, 685 us with 16 columns on
+// their way to registers while 16 are added.)
 #include <cooperative_groups.h>
 #include <stddef.h>
 #include <type_traits>
@@ -75,14 +76,14 @@ struct Shared {
 static_assert(offsetof(Shared, neg_lse) % 16 == 0, "16-byte reads");
 constexpr size_t kSmemBytes = 1024 + kRingOff + kRing * kStage + sizeof(Shared);
 
-// Adds exp2(s * scale + neg_lse) over 32 columns of scores; where kCut those
+// Adds exp2(s * scale + neg_lse) over 16 columns of scores; where kCut those
 // outside [c_lo, c_hi) are left out.
 template <bool kCut>
-__device__ __forceinline__ void add_chunk(const uint32_t (&v)[32], const float* neg_lse, uint64_t sc2, int c_lo,
+__device__ __forceinline__ void add_chunk(const uint32_t (&v)[16], const float* neg_lse, uint64_t sc2, int c_lo,
                                           int c_hi, uint64_t& acc0, uint64_t& acc1) {
   const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(neg_lse);
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < 4; ++c) {
     const ulonglong2 l = nl2[c];
     float e[4];
     f2_split(f2_fma(f2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), sc2, l.x), e[0], e[1]);
@@ -103,21 +104,25 @@ __device__ __forceinline__ float sum_pairs(uint64_t acc0, uint64_t acc1) {
   return (s0 + s1) + (s2 + s3);
 }
 
-// The same over the first `cols` columns of a tile; `release` is called when
-// the last are in registers.
+// The same over the first `cols` columns of a tile, 16 of them on their way
+// while 16 are added; `release` is called when the last are in registers.
 template <bool kCut, class Release>
 __device__ __forceinline__ float sum_tile(uint32_t tmem, const float* neg_lse, uint64_t sc2, int cols, int c_lo,
                                           int c_hi, Release release) {
   uint64_t acc0 = 0, acc1 = 0;                       // pairs of +0
   const int chunks = kCut ? (cols + 31) / 32 : 4;
+  uint32_t v[2][16];
+  tmem_ld16(tmem, v[0]);
 #pragma unroll
   for (int c4 = 0; c4 < 4; ++c4) {
     if (kCut && c4 >= chunks) break;
-    uint32_t v[32];
-    tmem_ld32(tmem + c4 * 32u, v);
     tc_wait_ld();
-    if (c4 == chunks - 1) release();
-    add_chunk<kCut>(v, neg_lse + c4 * 32, sc2, c_lo - c4 * 32, c_hi - c4 * 32, acc0, acc1);
+    tmem_ld16(tmem + c4 * 32u + 16u, v[1]);
+    add_chunk<kCut>(v[0], neg_lse + c4 * 32, sc2, c_lo - c4 * 32, c_hi - c4 * 32, acc0, acc1);
+    tc_wait_ld();
+    if (c4 + 1 < chunks) tmem_ld16(tmem + c4 * 32u + 32u, v[0]);
+    else release();
+    add_chunk<kCut>(v[1], neg_lse + c4 * 32 + 16, sc2, c_lo - c4 * 32 - 16, c_hi - c4 * 32 - 16, acc0, acc1);
   }
   return sum_pairs(acc0, acc1);
 }
@@ -171,8 +176,7 @@ key_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant
   // query rows that attend a key of the tile: [q_lo, q_hi), in tiles of 128 from q_lo
   const int obs0 = n - min(n, p.n_obs);
   const int q_lo = max(k0, obs0);
-  const int64_t reach = (int64_t)min(k0 + kTile, n) - 1 + p.window;
-  const int q_hi = reach < n ? (int)reach : n;
+  const int q_hi = min(n, min(k0 + kTile, n) - 1 + p.window);
   const int n_q = q_hi > q_lo ? (q_hi - q_lo + kTile - 1) / kTile : 0;
   const int n_all = n_q * p.ag_n[a];                 // tiles of every head
   const int n_x = n_all > rank ? (n_all - rank + n_ranks - 1) / n_ranks : 0;   // this CTA's: rank, rank + n_ranks, ...
@@ -289,9 +293,9 @@ key_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant
       tc_fence_after();
       // some pair of the tile is masked: a query before the tile's last key or past
       // the end, or a key out of a query's window (all observed: q0 >= q_lo)
-      const bool cut = q0 < k0 + kTile - 1 || q0 + kTile > q_hi || (int64_t)q0 + kTile - 1 - k0 >= p.window;
+      const bool cut = q0 < k0 + kTile - 1 || q0 + kTile > q_hi || q0 + kTile - 1 - k0 >= p.window;
       const int cols = min(kTile, q_hi - q0), c_lo = u - q0;
-      const int c_hi = (int)min((int64_t)(n - q0), (int64_t)u + p.window - q0);   // columns [c_lo, c_hi)
+      const int c_hi = min(n, u + p.window) - q0;    // columns [c_lo, c_hi)
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
@@ -335,7 +339,7 @@ constexpr int kKeyRing = 2;
 constexpr uint32_t kKeyOff = kMaxHalves / 2 * kStage;
 
 struct FewShared {
-  uint64_t q_full, q_empty, full[kKeyRing], empty[kKeyRing], s_full[kBufs], s_empty[kBufs], fin;
+  uint64_t q_full[kMaxHalves / 2], q_empty, full[kKeyRing], empty[kKeyRing], s_full[kBufs], s_empty[kBufs], fin;
   uint32_t tmem_base;
   int abort;
   // of warpgroup w: columns 32 w .. 32 w + 31 of every tile, log2 domain; read 16 bytes at a time
@@ -351,23 +355,23 @@ struct Unit {
   int obs0, per_head, halves, tiles;                 // first observed row; half tiles of one head and of all; tiles
   bool there, work;                                  // there are such keys; some observed row attends one
 };
-__device__ __forceinline__ Unit unit_at(const WeightParams& p, int64_t x, int64_t n_numbers) {
+__device__ __forceinline__ Unit unit_at(const WeightParams& p, int x, int n_numbers) {
   Unit u;
-  u.a = (int)(x / n_numbers);
+  u.a = x / n_numbers;
   u.there = packed_tile<kTile>(p.cu, p.S, p.T, x - u.a * n_numbers, &u.c0, &u.n, &u.k0);
   const int rows = min(u.n, p.n_obs);
   u.obs0 = u.n - rows;
   u.per_head = (rows + kHalf - 1) / kHalf;
   u.halves = u.per_head * p.ag_n[u.a];
   u.tiles = (u.halves + 1) / 2;
-  u.work = u.there && (int64_t)min(u.k0 + kTile, u.n) - 1 + p.window > u.obs0;
+  u.work = u.there && min(u.k0 + kTile, u.n) - 1 + p.window > u.obs0;
   return u;
 }
 // The unit behind u (number x): most often the next keys of the same sequence.
-__device__ __forceinline__ void next_unit(const WeightParams& p, int64_t x, int64_t n_numbers, Unit& u) {
+__device__ __forceinline__ void next_unit(const WeightParams& p, int x, int n_numbers, Unit& u) {
   if (u.there && u.k0 + kTile < u.n) {
     u.k0 += kTile;
-    u.work = (int64_t)min(u.k0 + kTile, u.n) - 1 + p.window > u.obs0;
+    u.work = min(u.k0 + kTile, u.n) - 1 + p.window > u.obs0;
   } else {
     u = unit_at(p, x, n_numbers);
   }
@@ -376,7 +380,7 @@ __device__ __forceinline__ void next_unit(const WeightParams& p, int64_t x, int6
 
 template <bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
-key_weights_few_kernel(const __grid_constant__ WeightParams p, int64_t n_numbers,
+key_weights_few_kernel(const __grid_constant__ WeightParams p, int n_numbers, int per_cta, int more,
                        const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, int* status) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -387,13 +391,12 @@ key_weights_few_kernel(const __grid_constant__ WeightParams p, int64_t n_numbers
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // units x0 .. x1 - 1, numbered KV head by KV head, so that neighbours mostly
   // share their queries
-  const int64_t n_units = n_numbers * p.n_ag;
-  const int64_t x0 = blockIdx.x * n_units / gridDim.x, x1 = (blockIdx.x + 1) * n_units / gridDim.x;
+  const int b = blockIdx.x, x0 = b * per_cta + min(b, more), x1 = x0 + per_cta + (b < more);
   // a wait runs out seconds after its block began, long after this
   if (blockIdx.x == 0 && tid == 0) *status = 0;
 
   if (tid == 0) {
-    mbar_init(smem_u32(&sh.q_full), 1);
+    for (int t = 0; t < kMaxHalves / 2; ++t) mbar_init(smem_u32(&sh.q_full[t]), 1);
     mbar_init(smem_u32(&sh.q_empty), 1);
     for (int s = 0; s < kKeyRing; ++s) {
       mbar_init(smem_u32(&sh.full[s]), 1);
@@ -426,44 +429,47 @@ key_weights_few_kernel(const __grid_constant__ WeightParams p, int64_t n_numbers
     }
     int m = 0, set = 0, c0 = -1, a = -1;
     Unit u = {};
-    for (int64_t x = x0; x < x1; ++x) {
+    for (int x = x0; x < x1; ++x) {
       next_unit(p, x, n_numbers, u);
       if (!u.work) continue;
-      if (u.c0 != c0 || u.a != a) {
-        if (set > 0) mbar_pass(smem_u32(&sh.q_empty), (set - 1) & 1, abort_flag);
-        if (__any_sync(0xffffffffu, *abort_flag)) break;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&sh.q_full);
-          mbar_arrive_expect_tx(bar, u.halves * (kStage / 2));
-          for (int f = 0; f < u.halves; ++f) {
-            const int h = p.head[p.ag_start[u.a] + f / u.per_head];
-            const int row = u.c0 + u.obs0 + f % u.per_head * kHalf;
-            const uint32_t dst = sb + (f >> 1) * kStage + (f & 1) * 8192u;
-            tma_load_4d(dst, &tmQ, bar, 0, h, row, 0);
-            tma_load_4d(dst + 16384, &tmQ, bar, 64, h, row, 0);
-          }
-        }
-        c0 = u.c0;
-        a = u.a;
-        ++set;
-      }
       const int s = m % kKeyRing;
       if (m >= kKeyRing) mbar_pass(smem_u32(&sh.empty[s]), (m / kKeyRing - 1) & 1, abort_flag);
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       if (lane == 0) {
         const uint32_t dst = sb + kKeyOff + s * kStage, bar = smem_u32(&sh.full[s]);
+        const int g = p.ag_kv[u.a], row = u.c0 + u.k0;
         mbar_arrive_expect_tx(bar, kStage);
-        tma_load_4d(dst, &tmK, bar, 0, p.ag_kv[u.a], u.c0 + u.k0, 0);
-        tma_load_4d(dst + 16384, &tmK, bar, 64, p.ag_kv[u.a], u.c0 + u.k0, 0);
+        tma_load_4d(dst, &tmK, bar, 0, g, row, 0);
+        tma_load_4d(dst + 16384, &tmK, bar, 64, g, row, 0);
       }
       ++m;
+      if (u.c0 != c0 || u.a != a) {
+        if (set > 0) mbar_pass(smem_u32(&sh.q_empty), (set - 1) & 1, abort_flag);
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        if (lane == 0) {
+          const int start = p.ag_start[u.a];
+          for (int f = 0, j = 0, part = 0; f < u.halves; ++f) {
+            const uint32_t bar = smem_u32(&sh.q_full[f >> 1]), dst = sb + (f >> 1) * kStage + (f & 1) * 8192u;
+            const int h = p.head[start + j], row = u.c0 + u.obs0 + part * kHalf;
+            if (!(f & 1)) mbar_arrive_expect_tx(bar, f + 1 < u.halves ? kStage : kStage / 2);
+            tma_load_4d(dst, &tmQ, bar, 0, h, row, 0);
+            tma_load_4d(dst + 16384, &tmQ, bar, 64, h, row, 0);
+            if (++part == u.per_head) { part = 0; ++j; }
+          }
+          for (int t = u.tiles; t < kMaxHalves / 2; ++t) mbar_arrive(smem_u32(&sh.q_full[t]));   // nothing there
+        }
+        c0 = u.c0;
+        a = u.a;
+        ++set;
+      }
     }
     if (lane == 0) {
       const long long t0 = clock64();
       while (!mbar_try_wait(smem_u32(&sh.fin), 0) && !*abort_flag && clock64() - t0 < kWaitLimitCycles) {
       }
       if (*abort_flag) {
-        if (set > 0) wait_short(smem_u32(&sh.q_full), (set - 1) & 1);
+        for (int t = 0; t < kMaxHalves / 2; ++t)
+          if (set > 0) wait_short(smem_u32(&sh.q_full[t]), (set - 1) & 1);
         for (int i = max(0, m - kKeyRing); i < m; ++i)
           wait_short(smem_u32(&sh.full[i % kKeyRing]), (i / kKeyRing) & 1);
       }
@@ -475,16 +481,17 @@ key_weights_few_kernel(const __grid_constant__ WeightParams p, int64_t n_numbers
     const uint64_t k_desc = desc_k_major(sb + kKeyOff), q_desc = desc_k_major(sb);
     int m = 0, set = 0, c0 = -1, a = -1;
     int i = 0;                                       // tiles
+    bool fresh = false;                              // queries that no product has read yet
     Unit u = {};
-    for (int64_t x = x0; x < x1; ++x) {
+    for (int x = x0; x < x1; ++x) {
       next_unit(p, x, n_numbers, u);
       if (!u.work) continue;
       if (u.c0 != c0 || u.a != a) {
         if (set > 0) commit_if(on, smem_u32(&sh.q_empty));     // the old queries' products are done
-        mbar_pass(smem_u32(&sh.q_full), set & 1, abort_flag);
         c0 = u.c0;
         a = u.a;
         ++set;
+        fresh = true;
       }
       const int s = m % kKeyRing;
       mbar_pass(smem_u32(&sh.full[s]), (m / kKeyRing) & 1, abort_flag);
@@ -492,6 +499,7 @@ key_weights_few_kernel(const __grid_constant__ WeightParams p, int64_t n_numbers
       for (int t = 0; t < u.tiles; ++t, ++i) {
         const int buf = i % kBufs;
         if (i >= kBufs) mbar_pass(smem_u32(&sh.s_empty[buf]), (i / kBufs - 1) & 1, abort_flag);
+        if (fresh) mbar_pass(smem_u32(&sh.q_full[t]), (set - 1) & 1, abort_flag);
         tc_fence_after();
         const uint64_t q_d = q_desc + (uint64_t)t * (kStage >> 4);
         if (2 * t + 1 < u.halves) issue_qk<F16>(on, tmem + buf * 128u, k_d, q_d);
@@ -499,6 +507,7 @@ key_weights_few_kernel(const __grid_constant__ WeightParams p, int64_t n_numbers
         commit_if(on, smem_u32(&sh.s_full[buf]));
       }
       commit_if(on, smem_u32(&sh.empty[s]));
+      fresh = false;
       ++m;
     }
     commit_if(on, smem_u32(&sh.fin));
@@ -514,7 +523,7 @@ key_weights_few_kernel(const __grid_constant__ WeightParams p, int64_t n_numbers
     int m = 0, c0 = -1, a = -1, i = 0;
     bool ok = true;              // after a wait that ran out a warp still meets the others at every barrier
     Unit u = {};
-    for (int64_t x = x0; x < x1; ++x) {
+    for (int x = x0; x < x1; ++x) {
       next_unit(p, x, n_numbers, u);
       if (!u.there) continue;
       const int key = u.k0 + r;
@@ -535,29 +544,49 @@ key_weights_few_kernel(const __grid_constant__ WeightParams p, int64_t n_numbers
         group_sync(wg);
       }
       uint64_t acc0 = 0, acc1 = 0;                   // pairs of +0
-      for (int t = 0; t < u.tiles; ++t, ++i) {
-        const int buf = i % kBufs;
-        const bool w = ok && mbar_spin(smem_u32(&sh.s_full[buf]), (i / kBufs) & 1, abort_flag);
+      // Queries q0 .. q0 + 31 are this warpgroup's columns of a tile (at: of its
+      // head's rows). 16 columns are on their way while 16 are added.
+      int at = (wg >> 1) * kHalf;
+      const int per_head = u.per_head * kHalf;
+      auto mine = [&](int t) {                       // some column is an observed row
+        while (at >= per_head) at -= per_head;
+        return 2 * t + (wg >> 1) < u.halves && u.obs0 + at + (wg & 1) * 32 < u.n;
+      };
+      auto ready = [&](int x) {
+        const bool w = ok && mbar_spin(smem_u32(&sh.s_full[x % kBufs]), (x / kBufs) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, w);
-        if (!ok) continue;
         tc_fence_after();
-        const int f = 2 * t + (wg >> 1);
-        const bool here = f < u.halves;              // this warpgroup's columns hold queries q0 .. q0 + 31
-        const int q0 = u.obs0 + (here ? f % u.per_head : 0) * kHalf + (wg & 1) * 32;
-        uint32_t v[32];
-        if (here && q0 < u.n) {
-          tmem_ld32(tmem + from + buf * 128u, v);
-          tc_wait_ld();
+      };
+      uint32_t v[2][16];
+      bool here = u.tiles > 0 && mine(0);
+      ready(i);
+      if (here) tmem_ld16(tmem + from + i % kBufs * 128u, v[0]);
+      for (int t = 0; t < u.tiles; ++t, ++i) {
+        const int q0 = u.obs0 + at + (wg & 1) * 32;
+        const bool cut = q0 < u.k0 + kTile - 1 || q0 + 32 > u.n || q0 + 31 - u.k0 >= p.window;
+        const int c_hi = min(u.n, key + p.window) - q0;
+        const bool now = here;
+        // two copies: with the mask as selects every tile would pay for it
+        auto add = [&](int half) {
+          if (cut) add_chunk<true>(v[half], nl + t * 32 + half * 16, sc2, key - q0 - half * 16, c_hi - half * 16, acc0, acc1);
+          else add_chunk<false>(v[half], nl + t * 32 + half * 16, sc2, 0, 16, acc0, acc1);
+        };
+        tc_wait_ld();
+        if (now) {
+          tmem_ld16(tmem + from + i % kBufs * 128u + 16u, v[1]);
+          add(0);
         }
+        tc_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.s_empty[buf]));
-        if (!here || q0 >= u.n) continue;
-        const bool cut = q0 < u.k0 + kTile - 1 || q0 + 32 > u.n || (int64_t)q0 + 31 - u.k0 >= p.window;
-        const int c_hi = (int)min((int64_t)(u.n - q0), (int64_t)key + p.window - q0);
-        // two copies: with the mask as selects every tile would pay for it
-        if (cut) add_chunk<true>(v, nl + t * 32, sc2, key - q0, c_hi, acc0, acc1);
-        else add_chunk<false>(v, nl + t * 32, sc2, 0, 32, acc0, acc1);
+        if (lane == 0) mbar_arrive(smem_u32(&sh.s_empty[i % kBufs]));
+        if (t + 1 < u.tiles) {
+          at += 2 * kHalf;
+          here = mine(t + 1);
+          ready(i + 1);
+          if (here) tmem_ld16(tmem + from + (i + 1) % kBufs * 128u, v[0]);
+        }
+        if (now) add(1);
       }
       // the warpgroups' sums, added in their order by each in turn
       float(*part)[kTile] = sh.part[m & 1];
@@ -611,7 +640,7 @@ cudaError_t launch_key_weights(const Tensor4& q, const Tensor4& k, bool f16, int
   if (!make_tmap_bnhd(&tk, k.p, 1, T, Hkv, 0, k.sn, k.sh, kTile)) return cudaErrorInvalidValue;
   WeightParams p;
   p.cu = cu; p.lse = lse; p.w = weights;
-  p.S = S; p.T = T; p.window = window; p.n_obs = n_obs;
+  p.S = S; p.T = T; p.window = window < T ? window : T; p.n_obs = n_obs;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.n_ag = 0;
   const int G = Hq / Hkv;
@@ -637,7 +666,8 @@ cudaError_t launch_key_weights(const Tensor4& q, const Tensor4& k, bool f16, int
     auto kernel = f16 ? key_weights_few_kernel<true> : key_weights_few_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmemBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(units < 148 ? units : 148), kThreads, kFewSmemBytes, stream>>>(p, n_numbers, tq, tk, status);
+    const int n_units = (int)units, grid = n_units < 148 ? n_units : 148;   // (fits: checked with the arguments)
+    kernel<<<grid, kThreads, kFewSmemBytes, stream>>>(p, (int)n_numbers, n_units / grid, n_units % grid, tq, tk, status);
     return cudaGetLastError();
   }
   if (!make_tmap_bnhd(&tq, q.p, 1, T, Hq, 0, q.sn, q.sh, kTile)) return cudaErrorInvalidValue;
