@@ -104,11 +104,15 @@ PACKED = [
     ([1000], 2, 1, 129, [0, 1], 9, 9, 0),
     ([640, 300], 4, 2, 128, [1, 3], 0, 0, 0),
     ([1500, 1, 64], 16, 1, None, [0, 15], 0, 0, 0),
-    # enough tiles that every CTA has its keys to itself; that two share them (fewer: three)
+    # many heads, or several prompts of a few tiles
     ([700, 65, 0, 300, 1, 129], 32, 4, None, list(range(32)), 0, 3, 0),
     ([700, 65, 0, 300, 1, 129], 32, 4, 100, list(range(32)), 1, 0, 0),
     ([600, 300, 500], 8, 2, None, list(range(8)), 0, 0, 8),
     ([600, 300, 500], 8, 2, 129, list(range(8)), 0, 0, 0),
+    # few units of many keys: three CTAs share a unit's keys, and two
+    ([900, 1500, 700], 2, 1, None, [1, 0], 2, 5, 0),
+    ([900, 1500, 700], 4, 1, None, list(range(4)), 0, 0, 8),
+    ([900, 1500, 700], 4, 2, 700, list(range(4)), 0, 0, 0),
     # short prompts and many tiles: one query tile a CTA; long ones: two
     ([1, 513, 0, 128, 2, 127, 256, 129, 16, 1], 32, 8, None, list(range(1, 32, 2)), 2, 200, 8),
     ([1, 513, 0, 128, 2, 127, 256, 129, 16, 1], 32, 8, 70, list(range(32)), 0, 0, 0),
