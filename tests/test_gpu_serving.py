@@ -710,6 +710,44 @@ def test_calls_on_two_streams():
         assert torch.equal(a, b)
 
 
+def test_kernels_of_every_kind_beside_each_other():
+    """Calls whose CTAs stay for many units, next to the other tensor-core
+    kernels, each on a stream of its own: the results of one after the other."""
+    dt = torch.bfloat16
+    (q1, k1, v1), _, cu1 = make_packed([100] * 200, 16, 4, dt, 81)
+    (q2, k2, v2), _, cu2 = make_packed([1500, 900, 1700, 1100], 16, 4, dt, 82)
+    gen = torch.Generator().manual_seed(83)
+    q3, k3, v3 = (rnd((1, 2048, h, D), dt, gen).to(DEV) for h in (8, 2, 2))
+    qt, kt = (rnd((1, h, 4096, 16), dt, gen).to(DEV) for h in (4, 2))
+    streams = [torch.cuda.Stream() for _ in range(5)]
+    ws = [torch.zeros(1 << 20, dtype=torch.uint8, device=DEV) for _ in streams]
+    lse = torch.zeros(16, q2.shape[0], device=DEV)
+    rtp.attn_packed(q2, k2, v2, torch.zeros_like(q2), list(range(16)), cu2, lse=lse)
+
+    def run(apart):
+        o1, o2, o3 = torch.zeros_like(q1), torch.zeros_like(q2), torch.zeros_like(q3)
+        w = torch.zeros(4, q2.shape[0], device=DEV)
+        blocks = torch.zeros(1, 4, 64, 16, dtype=torch.int32, device=DEV)
+        counts = torch.zeros(1, 4, 64, dtype=torch.int32, device=DEV)
+        calls = [lambda st, b: rtp.attn_packed(q1, k1, v1, o1, list(range(16)), cu1, ws=b, stream=st),
+                 lambda st, b: rtp.attn_packed(q2, k2, v2, o2, list(range(16)), cu2, ws=b, stream=st),
+                 lambda st, b: rtp.attn_key_weights(q2, k2, lse, w, list(range(16)), cu2, ws=b, stream=st),
+                 lambda st, b: rtp.swa(q3, k3, v3, o3, list(range(8)), 512, ws=b, stream=st),
+                 lambda st, b: rtp.select_prefill(qt, kt, [0, 0, 1, 1], 16, blocks, counts, ws=b, stream=st)]
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for call, stream, b in zip(calls, streams, ws):
+                call(stream if apart else None, b)
+                if not apart:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert all(rtp.workspace_status(b) == 0 for b in ws)
+        return o1, o2, o3, w, blocks, counts
+
+    for x, y in zip(run(False), run(True)):
+        assert torch.equal(x, y)
+
+
 def test_long_cache_offsets_pass_32_bits():
     """Page offsets beyond 2^31 elements (and 2^32 bytes) are addressed in 64 bits."""
     page, Hkv, pages = 256, 1, 70_000                       # 2.3e9 elements of k, as many of v
