@@ -32,6 +32,11 @@
 //   * With weights, the first kernel also stores the scaled scores (fp32, 4
 //     bytes against 512 / G per key and head) and a third kernel adds
 //     exp(score - lse) over the heads of a group, in a fixed order.
+//
+// Measured: 8 sequences of 131072 tokens, 32/4 heads, 332 us (6.5 TB/s, all of
+// what HBM gives a copy); 32 of 1 to 16385 tokens with weights, 58 us: 41 here
+// (start, ragged ends and score stores are on top of 27 of HBM), 2 the join, 12
+// the weights; one of 4099 tokens, window 1024, 8 us of the GPU's time.
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
@@ -46,7 +51,8 @@ constexpr int kCtasPerSm = 2;
 constexpr int kChunk = 64;                    // keys per chunk
 constexpr int kKeys = kChunk / kWarps;        // keys per warp and chunk
 constexpr int kStages = 3;
-// 32 sequences of 1 to 16385 tokens (32 / 4 heads): 61 us without it
+// 32 sequences of 1 to 16385 tokens (32 / 4 heads), weights and all: 57 us; 61
+// without it
 constexpr int kSegCost = 3;
 constexpr int kRowBytes = RTP_D * 2;
 constexpr int kSlab = kKeys * kRowBytes;      // one warp's K (or V) rows of one chunk

@@ -18,7 +18,7 @@
 //     bits are fewer, but every CTA then reads 64 KB of its neighbours'
 //     histograms a pass: 22 against 16 us for 8 x 4 rows of 5000 to 32768);
 //   * the move, bound by HBM: 512 bytes of K and V read and written per kept
-//     token and KV head.
+//     token and KV head (the same rows cut to 8192 each: 43 us, 6.2 TB/s).
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
