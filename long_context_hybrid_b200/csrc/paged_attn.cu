@@ -34,8 +34,8 @@
 //     exp(score - lse) over the heads of a group, in a fixed order.
 //
 // Measured: 8 sequences of 131072 tokens, 32/4 heads, 332 us (6.5 TB/s, all of
-// what HBM gives a copy); 32 of 1 to 16385 tokens with weights, 58 us: 41 here
-// (start, ragged ends and score stores are on top of 27 of HBM), 2 the join, 12
+// what HBM gives a copy); 32 of 1 to 16385 tokens with weights, 55 us: 41 here
+// (start, ragged ends and score stores are on top of 27 of HBM), 2 the join, 9
 // the weights; one of 4099 tokens, window 1024, 8 us of the GPU's time.
 #include <cooperative_groups.h>
 
@@ -51,8 +51,8 @@ constexpr int kCtasPerSm = 2;
 constexpr int kChunk = 64;                    // keys per chunk
 constexpr int kKeys = kChunk / kWarps;        // keys per warp and chunk
 constexpr int kStages = 3;
-// 32 sequences of 1 to 16385 tokens (32 / 4 heads), weights and all: 57 us; 61
-// without it
+// 32 sequences of 1 to 16385 tokens (32 / 4 heads), weights and all: 55 us with 2,
+// 3 or 4; 80 where beginnings do not count
 constexpr int kSegCost = 3;
 constexpr int kRowBytes = RTP_D * 2;
 constexpr int kSlab = kKeys * kRowBytes;      // one warp's K (or V) rows of one chunk
@@ -701,7 +701,9 @@ paged_join_kernel(const __grid_constant__ DecodeParams p) {
 // 256 slots form a list cut into equal runs, as above.
 namespace {
 constexpr int kWeightThreads = 256;
-constexpr int kWeightCtas = 148 * 8;
+// all at once; 32 sequences of 1 to 16385 tokens, the whole call: 55 us, with
+// 148 * 3 57, with 148 * 5 and 148 * 8 58
+constexpr int kWeightCtas = 148 * 4;
 struct SlotBlocks {
   static __device__ __forceinline__ int chunks(const DecodeParams& p, int b) {
     return (int)(((int64_t)seq_len(p.lens, b, p.max_len) + kWeightThreads - 1) / kWeightThreads);
