@@ -503,7 +503,10 @@ cudaError_t launch_cache_evict(const PagedView& src, const PagedView& dst, bool 
   int64_t n_keys = (most + ranks - 1) / ranks;
   if (n_keys > kSelKeys) n_keys = kSelKeys;
   const size_t smem = sizeof(SelectSmem) + (size_t)n_keys * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The limit is the function's, not the launch's: always the most that any call
+  // takes, so that a call in another host thread cannot lower it in between.
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(sizeof(SelectSmem) + kSelKeys * 4));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * ranks));

@@ -1,0 +1,70 @@
+"""What the serving calls promise beside their results: concurrent host threads,
+graphs, streams, empty batches, statuses and full caches, on the GPU."""
+import ctypes
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as SO
+from test_gpu_serving import D, DEV, _built, make_cache  # noqa: F401  (_built: the module's fixture)
+
+pytestmark = pytest.mark.gpu
+
+rtp = pytest.importorskip("long_context_hybrid_b200")
+
+
+def _struct(cache):
+    """The cache as the C ABI takes it."""
+    from long_context_hybrid_b200.serving import _CacheStruct
+    S = rtp.Strides
+    k, v, t = cache.k, cache.v, cache.table
+    return _CacheStruct(k.data_ptr(), v.data_ptr(), S(*k.stride()[:3]), S(*v.stride()[:3]), cache.weights.data_ptr(),
+                        t.data_ptr(), t.stride(0), k.shape[0], k.shape[1], t.shape[1], k.shape[2])
+
+
+def test_evictions_of_two_host_threads():
+    """Calls are reentrant: a small and a large eviction, issued side by side by
+    two host threads (the C calls run without the interpreter's lock), are each
+    accepted and each give what they give alone."""
+    jobs = []
+    for n, budget, seed in ((300, 100, 1), (400_000, 1000, 2)):
+        page = 256
+        pages = (n + page - 1) // page
+        gen = torch.Generator().manual_seed(seed)
+        k = torch.zeros(pages, page, 1, D, dtype=torch.bfloat16, device=DEV)
+        w = torch.rand(pages, 1, page, generator=gen).to(DEV)
+        table = torch.randperm(pages, generator=gen).to(torch.int32)[None].to(DEV)
+        src = rtp.PagedCache(k, k.clone(), table, w)
+        kept = (budget + page - 1) // page
+        dst = rtp.PagedCache(*(torch.zeros(kept, page, 1, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)),
+                             torch.arange(kept, dtype=torch.int32, device=DEV)[None],
+                             torch.zeros(kept, 1, page, device=DEV))
+        flat = w.cpu()[table[0].cpu().long(), 0].flatten()[:n].numpy()
+        jobs.append(dict(src=src, dst=dst, n=n, budget=budget, lens=torch.tensor([n], dtype=torch.int32, device=DEV),
+                         idx=torch.zeros(1, 1, budget, dtype=torch.int32, device=DEV),
+                         new=torch.zeros(1, dtype=torch.int32, device=DEV), stream=torch.cuda.Stream(),
+                         want=SO.evict_slots(flat, n, budget, 2, 10), bad=[]))
+    torch.cuda.synchronize()
+    call, gate = rtp.lib().rtp_cache_evict, threading.Barrier(len(jobs))
+
+    def work(j):
+        a, b = _struct(j["src"]), _struct(j["dst"])
+        gate.wait()
+        for _ in range(4000):
+            s = call(ctypes.byref(a), ctypes.byref(b), 1, j["lens"].data_ptr(), j["n"], j["budget"], 2, 10,
+                     j["idx"].data_ptr(), j["new"].data_ptr(), j["stream"].cuda_stream)
+            if s != 0:
+                j["bad"].append(s)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for j in jobs:
+        assert not j["bad"], f"{len(j['bad'])} calls refused, status {set(j['bad'])}"
+        assert np.array_equal(j["idx"].cpu().numpy()[0, 0], j["want"])
+        assert j["new"].tolist() == [j["budget"]]
