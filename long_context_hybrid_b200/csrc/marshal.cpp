@@ -51,6 +51,8 @@ struct Tensor {
   int64_t shape[kMaxDims], stride[kMaxDims];
   PyObject* dtype = nullptr;   // borrowed: torch's dtypes live as long as torch
   bool contiguous() const {
+    for (int d = 0; d < dims; ++d)
+      if (shape[d] == 0) return true;   // no element: strides say nothing
     int64_t want = 1;
     for (int d = dims - 1; d >= 0; --d) {
       if (shape[d] != 1 && stride[d] != want) return false;

@@ -68,3 +68,34 @@ def test_evictions_of_two_host_threads():
         assert not j["bad"], f"{len(j['bad'])} calls refused, status {set(j['bad'])}"
         assert np.array_equal(j["idx"].cpu().numpy()[0, 0], j["want"])
         assert j["new"].tolist() == [j["budget"]]
+
+
+def make_layer(B, capacity, Hq=4, Hkv=2, page=16, seed=0, **kw):
+    """A layer over zeroed pages in random order."""
+    gen = torch.Generator().manual_seed(seed)
+    pages = B * capacity // page
+    cache = rtp.PagedCache(*(torch.zeros(pages, page, Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)),
+                           torch.randperm(pages, generator=gen).to(torch.int32).view(B, -1).to(DEV),
+                           torch.zeros(pages, Hkv, page, device=DEV))
+    return rtp.PagedLayer(cache, Hq, **kw), gen
+
+
+def rows(gen, n, H, scale=1.0):
+    return (torch.randn(n, H, D, generator=gen) * scale).to(torch.bfloat16).to(DEV)
+
+
+def test_empty_prompts():
+    """A batch of empty prompts: nothing is attended, weighed or cached, and
+    decoding goes on from length 0."""
+    B = 3
+    layer, gen = make_layer(B, 32)
+    layer.lens.fill_(5)
+    q, kv = rows(gen, 0, 4), rows(gen, 0, 2)
+    cu = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    layer.prefill(q, kv, kv, torch.zeros_like(q), cu)
+    assert layer.lens.tolist() == [0] * B and not layer.cache.weights.any()
+    q1, k1, v1 = rows(gen, B, 4), rows(gen, B, 2), rows(gen, B, 2)
+    o1 = torch.zeros_like(q1)
+    layer.decode(q1, k1, v1, o1)
+    assert torch.equal(o1, v1.repeat_interleave(2, dim=1))     # one key: its value
+    assert layer.lens.tolist() == [1] * B

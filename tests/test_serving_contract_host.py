@@ -1,0 +1,66 @@
+"""CPU checks of what the serving calls promise: argument marshalling seen
+through stand-in tensors (nothing here reaches a device)."""
+import ctypes
+
+import pytest
+import torch
+
+from long_context_hybrid_b200 import serving
+
+FAKE = 0x10000                                  # never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def rtp():
+    from long_context_hybrid_b200 import build
+    build.build()
+    import long_context_hybrid_b200 as rtp
+    rtp.lib()
+    return rtp
+
+
+class OnGpu:
+    """A CPU tensor's layout under a device number and an address."""
+
+    def __init__(self, t, address=FAKE):
+        self.t, self.address, self.dtype, self.shape = t, address, t.dtype, t.shape
+
+    def stride(self):
+        return self.t.stride()
+
+    def data_ptr(self):
+        return self.address
+
+    def get_device(self):
+        return 0
+
+
+@pytest.fixture
+def native(rtp, monkeypatch):
+    """The native module with device 0 current, whatever the machine has."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(serving, "_native", None)
+    yield serving._marshal()
+    monkeypatch.undo()
+    serving._native = None                       # set up again at the next call
+
+
+def test_tensors_without_rows_are_contiguous(rtp, native):
+    """T = 0 with several listed heads: the empty lse and weights are taken as
+    they are, and the call goes on to the C checks (a misaligned workspace ends
+    it there)."""
+    q, k = (OnGpu(torch.zeros(0, h, 128, dtype=torch.bfloat16)) for h in (4, 2))
+    cu = OnGpu(torch.zeros(4, dtype=torch.int32))
+    lse, w = OnGpu(torch.zeros(3, 0)), OnGpu(torch.zeros(2, 0))
+    ws = OnGpu(torch.zeros(256, dtype=torch.uint8), FAKE + 16)
+    heads = serving._head_bytes((0, 1, 3))
+    with pytest.raises(rtp.RtpError, match="RTP_ERR_WORKSPACE"):
+        native.attn_packed(q, k, k, q, heads, cu, None, None, lse, ws, 0)
+    with pytest.raises(rtp.RtpError, match="RTP_ERR_WORKSPACE"):
+        native.attn_key_weights(q, k, lse, w, heads, cu, None, None, None, ws, 0)
+    with pytest.raises(rtp.RtpError, match="contiguous"):         # the shape is still checked
+        native.attn_packed(q, k, k, q, heads, cu, None, None, OnGpu(torch.zeros(2, 0)), ws, 0)
+    strided = OnGpu(torch.zeros(3, 8)[:, ::2])
+    q5, k5 = (OnGpu(torch.zeros(4, h, 128, dtype=torch.bfloat16)) for h in (4, 2))
+    with pytest.raises(rtp.RtpError, match="contiguous"):         # and so is the layout of what has rows
+        native.attn_packed(q5, k5, k5, q5, heads, cu, None, None, strided, ws, 0)
