@@ -158,7 +158,8 @@ def attn_packed(q, k, v, o, heads: Sequence[int], cu_seqlens, window: Optional[i
     """Causal attention of packed prompts: q/o [T,Hq,D], k/v [T,Hkv,D],
     ``cu_seqlens`` int32 [S+1] on the device; writes o[:, heads] (rows of
     sequences) and ``lse`` fp32 [len(heads), T]. ``window`` None: the whole
-    prefix."""
+    prefix. ``ws``: 256 bytes of the caller's; give them to read the call's
+    status afterwards (``workspace_status``)."""
     ws = _empty(256, torch.uint8, q, stream) if ws is None else _bytes(ws)
     _call("attn_packed", q, q, k, v, o, _head_bytes(tuple(heads)), cu_seqlens, window, scale, lse, ws,
           None if stream is None else stream.cuda_stream)
@@ -171,7 +172,7 @@ def attn_key_weights(q, k, lse, weights, heads: Sequence[int], cu_seqlens, n_obs
     """The attention weight each key of packed prompts got from the last
     ``n_obs`` rows of its sequence (None: every row), summed over the listed
     heads of its KV head, into ``weights`` fp32 [Hkv, T]; ``lse`` fp32
-    [len(heads), T] from ``attn_packed``."""
+    [len(heads), T] from ``attn_packed``; ``ws`` as there."""
     ws = _empty(256, torch.uint8, q, stream) if ws is None else _bytes(ws)
     _call("attn_key_weights", q, q, k, lse, weights, _head_bytes(tuple(heads)), cu_seqlens, n_obs, window, scale, ws,
           None if stream is None else stream.cuda_stream)
@@ -257,7 +258,9 @@ class PagedLayer:
         B, dev = cache.table.shape[0], cache.k.device
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
         self.cu_decode = torch.arange(B + 1, dtype=torch.int32, device=dev)
-        self.ws_prefill = torch.zeros(256, dtype=torch.uint8, device=dev)
+        # a status word of its own for every tensor-core call of a prefill: the
+        # kernels clear the one they are given
+        self.ws_prefill = torch.zeros(len(self._groups()), 2, 256, dtype=torch.uint8, device=dev)
         weighed = cache.weights is not None
         self.ws = torch.empty(max(decode_workspace_size(B, cache.capacity, len(g), w, sink, weighed)
                                   for g, w in self._groups()), dtype=torch.uint8, device=dev)
@@ -270,15 +273,14 @@ class PagedLayer:
         """q/o [T,Hq,D], k/v [T,Hkv,D] of B packed prompts (one per table row)."""
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.k.device)):
             weights = None
-            for heads, window in self._groups():
+            for (heads, window), ws in zip(self._groups(), self.ws_prefill):
                 lse = None
                 if self.cache.weights is not None:
                     lse = torch.empty(len(heads), q.shape[0], dtype=torch.float32, device=q.device)
-                attn_packed(q, k, v, o, heads, cu_seqlens, window, self.scale, lse, self.ws_prefill)
+                attn_packed(q, k, v, o, heads, cu_seqlens, window, self.scale, lse, ws[0])
                 if lse is not None:
                     w = torch.zeros(k.shape[1], k.shape[0], dtype=torch.float32, device=q.device)
-                    attn_key_weights(q, k, lse, w, heads, cu_seqlens, self.n_obs, window, self.scale,
-                                     self.ws_prefill)
+                    attn_key_weights(q, k, lse, w, heads, cu_seqlens, self.n_obs, window, self.scale, ws[1])
                     weights = w if weights is None else weights.add_(w)
             self.lens.zero_()
             paged_append(self.cache, k, v, cu_seqlens, self.lens, weights)
@@ -302,3 +304,13 @@ class PagedLayer:
             idx, new_lens = cache_evict(self.cache, self.lens, budget, self.sink, recent)
             self.lens.copy_(new_lens)
         return idx
+
+    def device_status(self, stream=None) -> int:
+        """Synchronises and returns the worst status word of the last prefill's
+        attention and key-weight calls (0 = RTP_OK, 4 = RTP_ERR_TIMEOUT: rows of
+        ``o`` and weights in the cache are missing). The other calls never wait
+        on the device and report nothing there."""
+        import long_context_hybrid_b200 as base
+        dev = self.cache.k.device
+        with torch.cuda.stream(stream or torch.cuda.current_stream(dev)):
+            return max(base.workspace_status(ws) for ws in self.ws_prefill.flatten(0, 1))

@@ -99,3 +99,36 @@ def test_empty_prompts():
     layer.decode(q1, k1, v1, o1)
     assert torch.equal(o1, v1.repeat_interleave(2, dim=1))     # one key: its value
     assert layer.lens.tolist() == [1] * B
+
+
+@pytest.mark.parametrize("late", [0, 1, 2, 3])
+def test_a_prefills_status_survives_its_later_calls(monkeypatch, late):
+    """A prefill of full and streaming heads makes four tensor-core calls. A
+    status that one of them leaves (planted here) is still there at the end, and
+    gone after the next prefill."""
+    from long_context_hybrid_b200 import serving
+    layer, gen = make_layer(2, 64, streaming=[1], window=8, sink=1)
+    lens = [20, 7]
+    q, k, v = rows(gen, 27, 4), rows(gen, 27, 2), rows(gen, 27, 2)
+    cu = torch.tensor([0, 20, 27], dtype=torch.int32, device=DEV)
+    made = []
+
+    def planting(call):
+        def wrapped(*args):
+            call(*args)
+            if len(made) == late:
+                args[-1].view(torch.int32)[0] = 4
+            made.append(call)
+        return wrapped
+
+    o = torch.zeros_like(q)
+    with monkeypatch.context() as m:
+        for name in ("attn_packed", "attn_key_weights"):
+            m.setattr(serving, name, planting(getattr(serving, name)))
+        layer.prefill(q, k, v, o, cu)
+    assert len(made) == 4
+    assert layer.device_status() == 4 and layer.device_status(torch.cuda.Stream()) == 4
+    layer.decode(rows(gen, 2, 4), rows(gen, 2, 2), rows(gen, 2, 2), rows(gen, 2, 4))
+    assert layer.device_status() == 4
+    layer.prefill(q, k, v, o, cu)
+    assert layer.device_status() == 0 and layer.lens.tolist() == lens
