@@ -244,6 +244,11 @@ class PagedLayer:
     the cache; ``decode`` appends one token per sequence and attends;
     ``evict`` shrinks the cache in place. ``lens`` is the device's record of
     the sequences' lengths, kept by these calls; buffers are kept across calls.
+
+    A token beyond the cache's capacity finds no slot: it is dropped, counted in
+    ``lens`` (the calls clamp it) until ``evict`` makes room, and reported by
+    ``dropped()``. Rows of such a sequence attend what fits, without the token
+    itself: evict, or end the sequence, before ``lens`` reaches the capacity.
     """
 
     def __init__(self, cache: PagedCache, Hq: int, streaming: Sequence[int] = (), window: Optional[int] = None,
@@ -257,6 +262,7 @@ class PagedLayer:
         self.scale = scale
         B, dev = cache.table.shape[0], cache.k.device
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        self._dropped = torch.zeros_like(self.lens)   # tokens without a slot, up to the last eviction
         self.cu_decode = torch.arange(B + 1, dtype=torch.int32, device=dev)
         # a status word of its own for every tensor-core call of a prefill: the
         # kernels clear the one they are given
@@ -283,6 +289,7 @@ class PagedLayer:
                     attn_key_weights(q, k, lse, w, heads, cu_seqlens, self.n_obs, window, self.scale, ws[1])
                     weights = w if weights is None else weights.add_(w)
             self.lens.zero_()
+            self._dropped.zero_()
             paged_append(self.cache, k, v, cu_seqlens, self.lens, weights)
             torch.sub(cu_seqlens[1:], cu_seqlens[:-1], out=self.lens)
         return o
@@ -302,8 +309,18 @@ class PagedLayer:
         ``sink`` first and ``recent`` last; returns the kept slots."""
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.k.device)):
             idx, new_lens = cache_evict(self.cache, self.lens, budget, self.sink, recent)
+            self._dropped.add_(self._beyond())
             self.lens.copy_(new_lens)
         return idx
+
+    def _beyond(self) -> torch.Tensor:
+        return (self.lens - self.cache.capacity).clamp_(min=0)
+
+    def dropped(self, stream=None) -> torch.Tensor:
+        """int32 [B] on the device: the tokens of each sequence that found no
+        slot since its prefill."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.cache.k.device)):
+            return self._dropped + self._beyond()
 
     def device_status(self, stream=None) -> int:
         """Synchronises and returns the worst status word of the last prefill's

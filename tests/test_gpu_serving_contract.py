@@ -132,3 +132,33 @@ def test_a_prefills_status_survives_its_later_calls(monkeypatch, late):
     assert layer.device_status() == 4
     layer.prefill(q, k, v, o, cu)
     assert layer.device_status() == 0 and layer.lens.tolist() == lens
+
+
+def test_tokens_beyond_the_capacity_are_reported():
+    """A full sequence: what finds no slot is dropped and counted, in prompts and
+    in decoding, before and after an eviction; nobody else's pages change."""
+    B, cap = 3, 32
+    layer, gen = make_layer(B, cap)
+    lens = [40, 31, 3]
+    q, k, v = (rows(gen, sum(lens), h) for h in (4, 2, 2))
+    cu = torch.tensor([0, 40, 71, 74], dtype=torch.int32, device=DEV)
+    layer.prefill(q, k, v, torch.zeros_like(q), cu)
+    assert layer.dropped().tolist() == [8, 0, 0]
+    cached = lambda b, n: layer.cache.k[layer.cache.table[b].long()].flatten(0, 1)[:n]  # noqa: E731
+    for b, n in enumerate([32, 31, 3]):
+        assert torch.equal(cached(b, n), k[cu[b]:cu[b] + n])
+    new = []
+    for step in range(3):
+        q1, k1, v1 = (rows(gen, B, h) for h in (4, 2, 2))
+        new.append(k1)
+        layer.decode(q1, k1, v1, torch.zeros_like(q1))
+    assert layer.dropped().tolist() == [11, 2, 0]
+    assert torch.equal(cached(0, 32), k[:32])
+    assert torch.equal(cached(1, 32), torch.cat([k[40:71], new[0][1:2]]))
+    assert torch.equal(cached(2, 6), torch.cat([k[71:74]] + [x[2:3] for x in new]))
+    layer.evict(20, 10)
+    assert layer.lens.tolist() == [20, 20, 6] and layer.dropped().tolist() == [11, 2, 0]
+    layer.decode(q1, k1, v1, torch.zeros_like(q1))
+    assert layer.lens.tolist() == [21, 21, 7] and layer.dropped().tolist() == [11, 2, 0]
+    layer.prefill(q, k, v, torch.zeros_like(q), cu)
+    assert layer.dropped().tolist() == [8, 0, 0]
