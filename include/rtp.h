@@ -660,7 +660,9 @@ RTP_API rtp_status rtp_paged_append(const rtp_paged_cache* cache, const void* k,
  *   ws       rtp_workspace_size_paged_attn_decode(B, max_len, n_heads, window,
  *            sink, weights_out != NULL) bytes; the status word always reads
  *            RTP_OK (the kernels never wait on one another on the device).
- *   Hq / Hkv <= 16, Hq <= 256, 1 <= B <= 65535, window >= 1, sink >= 0, 0 < scale < 1e38.
+ *   Hq / Hkv <= 16, Hq <= 256, 1 <= B <= 65535, window >= 1, sink >= 0, 0 < scale < 1e38;
+ *   min(B, 128) * (n / 64 + 4) < 2^31, n = min(max_len, sink + window) (128
+ *   sequences that could attend 2^30 slots each are refused).
  */
 RTP_API size_t rtp_workspace_size_paged_attn_decode(int B, int max_len, int n_heads, int window, int sink,
                                                     int with_weights);

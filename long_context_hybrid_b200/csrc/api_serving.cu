@@ -159,6 +159,7 @@ rtp_status rtp_paged_attn_decode(const void* q, rtp_strides qs, const rtp_paged_
   if (weights_out && !cache->weights) return RTP_ERR_INVALID_ARG;
   if ((st = check_heads(heads, n_heads, Hq)) != RTP_OK) return st;
   if (Hq > 256 || Hq / view.Hkv > 16 || B > 65535) return RTP_ERR_UNSUPPORTED;
+  if (!paged_decode_countable(B, max_len, window, sink)) return RTP_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(o)) return RTP_ERR_INVALID_ARG;
   if (!step_ok(qs.b, B) || !step_ok(qs.h, Hq) || !step_ok(os.b, B) || !step_ok(os.h, Hq)) return RTP_ERR_INVALID_ARG;
   const size_t need = paged_decode_ws_bytes(B, max_len, n_heads, window, sink, weights_out != nullptr);

@@ -771,6 +771,13 @@ int64_t attended_cap(int max_len, int window, int sink) {
 constexpr int kMaxCtas = 148 * kCtasPerSm;     // partials are sized for this many
 }  // namespace
 
+// LenScan adds up the units of a block's sequences in an int. (The slot blocks of
+// the weights kernel are fewer: 256 sequences of at most 2^22.)
+bool paged_decode_countable(int B, int max_len, int window, int sink) {
+  const int64_t units = attended_cap(max_len, window, sink) / kChunk + kSegCost;
+  return (B < kThreads ? B : kThreads) * units <= INT32_MAX;
+}
+
 size_t paged_decode_ws_bytes(int B, int max_len, int n_heads, int window, int sink, bool weights) {
   const int rows = n_heads < kGroup ? n_heads : kGroup;
   size_t n = kHeaderBytes + up256((size_t)2 * kMaxCtas * rows * kPart * sizeof(float));

@@ -164,6 +164,7 @@ cudaError_t launch_cache_evict(const PagedView& src, const PagedView& dst, bool 
 
 // One new token per sequence over the paged cache; heads sorted by KV head.
 size_t paged_decode_ws_bytes(int B, int max_len, int n_heads, int window, int sink, bool weights);
+bool paged_decode_countable(int B, int max_len, int window, int sink);   // the split's sums fit their type
 cudaError_t launch_paged_decode(const PagedView& c, const void* q, int64_t q_sb, int64_t q_sh, void* o, int64_t o_sb,
                                 int64_t o_sh, bool f16, int B, int G, const int32_t* heads, int n_heads,
                                 const int32_t* lens, int max_len, int window, int sink, float scale, float* lse,

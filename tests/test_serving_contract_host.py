@@ -64,3 +64,26 @@ def test_tensors_without_rows_are_contiguous(rtp, native):
     q5, k5 = (OnGpu(torch.zeros(4, h, 128, dtype=torch.bfloat16)) for h in (4, 2))
     with pytest.raises(rtp.RtpError, match="contiguous"):         # and so is the layout of what has rows
         native.attn_packed(q5, k5, k5, q5, heads, cu, None, None, strided, ws, 0)
+
+
+def test_decode_refuses_what_its_split_cannot_count(rtp):
+    """The split counts the 64-slot chunks of up to 128 sequences in 32 bits:
+    128 sequences of 2^30 attended slots are refused before the workspace is
+    looked at, 127 of them or a window that bounds them are not."""
+    S = rtp.Strides
+    c = serving._CacheStruct(FAKE, FAKE, S(65536 * 128, 128, 128), S(65536 * 128, 128, 128), FAKE, FAKE, 1 << 14, 10,
+                             65536, 1 << 14, 1)
+    heads = (ctypes.c_int32 * 1)(0)
+
+    def decode(B, max_len=1 << 30, window=2 ** 31 - 1, sink=0, ws=None):
+        return rtp.lib().rtp_paged_attn_decode(FAKE, S(128, 0, 128), c, FAKE, max_len, FAKE, S(128, 0, 128), 0, B, 1,
+                                               heads, 1, window, sink, ctypes.c_float(0.1), None, None, ws, 1 << 40,
+                                               None)
+
+    unsupported, workspace = 2, 5
+    for B in (128, 129, 65535):
+        assert decode(B) == unsupported, B
+        assert decode(B, window=1 << 29, sink=1 << 29) == unsupported, B
+        assert decode(B, window=1 << 20) == workspace, B
+        assert decode(B, max_len=1 << 29) == workspace, B
+    assert decode(127) == workspace
