@@ -4,7 +4,9 @@
 
 Every ``csrc/*.cu`` is compiled for sm_100a with nvcc (in parallel), then
 linked into one shared library with the CUDA runtime linked statically.
-``csrc/marshal.cpp`` becomes the Python module ``_marshal`` beside it.
+``csrc/marshal.cpp`` becomes the Python module ``_marshal`` beside it; where
+Python's headers are missing the library is built alone (it needs neither), with
+a warning, and the package's serving calls say what they miss.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -52,10 +55,15 @@ def _inputs():
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def _has_python_headers() -> bool:
+    return os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(OUT) or not os.path.exists(MARSHAL):
+    outputs = [OUT, MARSHAL] if _has_python_headers() else [OUT]
+    if not all(os.path.exists(f) for f in outputs):
         return False
-    t = min(os.path.getmtime(OUT), os.path.getmtime(MARSHAL))
+    t = min(os.path.getmtime(f) for f in outputs)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -69,6 +77,11 @@ def _compile(src: str) -> str:
 
 
 def _marshal() -> None:
+    if not _has_python_headers():
+        warnings.warn("Python.h not found: librtp.so is built without the Python module of the serving calls")
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)                   # of an earlier library
+        return
     tmp = MARSHAL + ".tmp"
     cmd = [cxx(), "-std=c++17", "-O2", "-Wall", "-fPIC", "-fvisibility=hidden", "-fno-exceptions", "-shared",
            "-static-libgcc", "-static-libstdc++", "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", tmp]
@@ -85,13 +98,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         module = ex.submit(_marshal)
         objs = list(ex.map(_compile, sources()))
-        module.result()
     tmp = OUT + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OUT)
+    module.result()                              # after the library, which does not need it
     if verbose:
         print(f"built {OUT}")
     return OUT

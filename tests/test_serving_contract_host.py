@@ -87,3 +87,34 @@ def test_decode_refuses_what_its_split_cannot_count(rtp):
         assert decode(B, window=1 << 20) == workspace, B
         assert decode(B, max_len=1 << 29) == workspace, B
     assert decode(127) == workspace
+
+
+@pytest.fixture
+def small_build(tmp_path, monkeypatch):
+    """The build over one small source, into a folder of its own."""
+    from long_context_hybrid_b200 import build
+    src = tmp_path / "one.cu"
+    src.write_text('extern "C" __attribute__((visibility("default"))) int one() { return 1; }\n')
+    for name, value in (("OUT", tmp_path / "librtp.so"), ("MARSHAL", tmp_path / "_marshal.so"),
+                        ("BUILD_DIR", tmp_path / "_build")):
+        monkeypatch.setattr(build, name, str(value))
+    monkeypatch.setattr(build, "sources", lambda: [str(src)])
+    return build
+
+
+def test_library_builds_without_python_headers(small_build, tmp_path, monkeypatch):
+    real = small_build.sysconfig.get_paths()
+    monkeypatch.setattr(small_build.sysconfig, "get_paths", lambda: {**real, "include": str(tmp_path / "none")})
+    (tmp_path / "_marshal.so").write_text("of an earlier library")
+    with pytest.warns(UserWarning, match="Python.h"):
+        small_build.build(force=True)
+    assert ctypes.CDLL(small_build.OUT).one() == 1 and not (tmp_path / "_marshal.so").exists()
+    assert small_build.up_to_date()
+
+
+def test_library_is_there_although_the_module_fails(small_build, tmp_path, monkeypatch):
+    monkeypatch.setattr(small_build, "cxx", lambda: "false")
+    with pytest.raises(RuntimeError, match="marshal.cpp"):
+        small_build.build()
+    assert ctypes.CDLL(small_build.OUT).one() == 1
+    assert not small_build.up_to_date()                          # the module is still to be built
