@@ -243,7 +243,9 @@ class PagedLayer:
     cache has weights, the weights that their last ``n_obs`` queries gave) into
     the cache; ``decode`` appends one token per sequence and attends;
     ``evict`` shrinks the cache in place. ``lens`` is the device's record of
-    the sequences' lengths, kept by these calls; buffers are kept across calls.
+    the sequences' lengths, kept by these calls; buffers are kept across calls,
+    so the calls of a layer (and replays of graphs that hold them) come one after
+    the other: on one stream, or on streams that wait for each other.
 
     A token beyond the cache's capacity finds no slot: it is dropped, counted in
     ``lens`` (the calls clamp it) until ``evict`` makes room, and reported by
@@ -270,6 +272,8 @@ class PagedLayer:
         weighed = cache.weights is not None
         self.ws = torch.empty(max(decode_workspace_size(B, cache.capacity, len(g), w, sink, weighed)
                                   for g, w in self._groups()), dtype=torch.uint8, device=dev)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()     # the calls may come on any stream
 
     def _groups(self):
         """(heads, window) of the two kinds of heads that are there."""

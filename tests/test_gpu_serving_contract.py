@@ -162,3 +162,21 @@ def test_tokens_beyond_the_capacity_are_reported():
     assert layer.lens.tolist() == [21, 21, 7] and layer.dropped().tolist() == [11, 2, 0]
     layer.prefill(q, k, v, torch.zeros_like(q), cu)
     assert layer.dropped().tolist() == [8, 0, 0]
+
+
+def test_a_layers_buffers_are_ready_on_every_stream():
+    """A layer made on a stream that is still busy, used on another at once."""
+    busy, other = torch.cuda.Stream(), torch.cuda.Stream()
+    ready, gen = make_layer(2, 32)
+    q, k, v = (rows(gen, 2, h) for h in (4, 2, 2))
+    o = torch.zeros_like(q)
+    ready.decode(q, k, v, o, stream=other)       # every kernel is loaded before the sleep
+    ready.cache.k.zero_(), ready.cache.v.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(400_000_000)           # about a fifth of a second
+        layer = rtp.PagedLayer(ready.cache, 4)
+    layer.decode(q, k, v, o, stream=other)
+    torch.cuda.synchronize()
+    assert layer.lens.tolist() == [1, 1] and layer.cu_decode.tolist() == [0, 1, 2]
+    assert torch.equal(o, v.repeat_interleave(2, dim=1))
