@@ -655,8 +655,8 @@ RTP_API rtp_status rtp_paged_append(const rtp_paged_cache* cache, const void* k,
  *   weights_out  fp32 like cache->weights, or NULL: for every slot s < len and
  *            every KV head with a listed head, weights_out = cache->weights +
  *            the sum over the group's listed heads of the softmax weight of s
- *            (0 where s is not attended). May be cache->weights itself. Pages
- *            may then not be shared between the sequences of a call.
+ *            (0 where s is not attended). May be cache->weights itself. With it
+ *            no page may be shared by sequences of a call or named twice by one.
  *   ws       rtp_workspace_size_paged_attn_decode(B, max_len, n_heads, window,
  *            sink, weights_out != NULL) bytes; the status word always reads
  *            RTP_OK (the kernels never wait on one another on the device).
@@ -681,11 +681,17 @@ RTP_API rtp_status rtp_paged_attn_decode(const void* q, rtp_strides qs, const rt
  *   NaN ranks above every number). Kept slot number j (ascending) moves to
  *   slot j: its K and V rows and its weight. Shorter sequences keep everything.
  *   Heads keep different tokens, so afterwards a slot is no longer a position;
- *   keys are expected with their positions already applied.
+ *   keys are expected with their positions already applied, and a window of
+ *   rtp_paged_attn_decode counts slots: its last slots are the last positions
+ *   only as far as `recent` reaches.
+ *   Every slot below len should hold a token. One whose page is missing ranks
+ *   behind every token; kept all the same (in {0 .. sink-1}, in the last
+ *   `recent`, or for want of others), it moves nothing: slot j, which counts as
+ *   a token afterwards, is left as it was.
  *
  *   src, dst host structs, both with weights. dst == src, or an equal struct,
  *            works in place (slots behind budget keep their old contents, and
- *            sequences may not share pages); otherwise the pages that dst's
+ *            no page may be shared or named twice); otherwise the pages that dst's
  *            table names may not be among src's, and dst needs capacity for
  *            min(budget, max_len) slots. The same table with only some of the
  *            buffers shared is refused. dst may have another page size.

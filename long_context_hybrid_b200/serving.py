@@ -220,9 +220,11 @@ def cache_evict(cache: PagedCache, lens, budget: int, sink: int = 0, recent: int
                 new_lens: Optional[torch.Tensor] = None, max_len: Optional[int] = None, stream=None):
     """Shrinks the cache to ``budget`` tokens per sequence and KV head: the
     first ``sink``, the last ``recent`` and the others of largest accumulated
-    weight, moved to slots 0, 1, ... of ``out`` (default: in place). Returns
-    (idx int32 [B,Hkv,budget], the kept slots ascending and -1 padded; new_lens
-    int32 [B])."""
+    weight, moved to slots 0, 1, ... of ``out`` (default: in place; no page may
+    then be shared). Every slot below a length should hold a token: one whose
+    page is missing ranks last and, kept all the same, leaves its new slot as it
+    was. Afterwards a slot is no longer a position. Returns (idx int32
+    [B,Hkv,budget], the kept slots ascending and -1 padded; new_lens int32 [B])."""
     if out is None:
         out = cache
     if idx is None:
@@ -242,7 +244,9 @@ class PagedLayer:
     ``prefill`` runs packed prompts and puts their keys and values (and, if the
     cache has weights, the weights that their last ``n_obs`` queries gave) into
     the cache; ``decode`` appends one token per sequence and attends;
-    ``evict`` shrinks the cache in place. ``lens`` is the device's record of
+    ``evict`` shrinks the cache in place; from then on the ``window`` of the
+    streaming heads counts slots, of which the last ``recent`` and those decoded
+    since are the last positions. ``lens`` is the device's record of
     the sequences' lengths, kept by these calls; buffers are kept across calls,
     so the calls of a layer (and replays of graphs that hold them) come one after
     the other: on one stream, or on streams that wait for each other.

@@ -180,3 +180,45 @@ def test_a_layers_buffers_are_ready_on_every_stream():
     torch.cuda.synchronize()
     assert layer.lens.tolist() == [1, 1] and layer.cu_decode.tolist() == [0, 1, 2]
     assert torch.equal(o, v.repeat_interleave(2, dim=1))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_eviction_around_missing_pages(in_place):
+    """Slots whose page is missing rank behind every token, move nothing and
+    leave their new slot as it was; all the others move as ever."""
+    lens, page, budget, sink, recent, Hkv = [300, 90], 16, 64, 20, 20, 2
+    cache, gen = make_cache(lens, Hkv, page, torch.bfloat16, 15)
+    for b, j, bad in ((0, 1, -1), (0, 7, 10 ** 6), (1, 0, -2 ** 31), (1, 3, cache.num_pages), (0, 18, -1)):
+        cache.table[b, j] = bad                  # in the sink, among the candidates, at the end
+    table = cache.table.cpu().long()
+    there = (table >= 0) & (table < cache.num_pages)
+    old = [x.cpu() for x in (cache.k, cache.v)]
+    old_w = cache.weights.cpu()
+    out = cache
+    if not in_place:
+        out, _ = make_cache([budget] * 2, Hkv, 32, torch.bfloat16, 16)
+        for x in (out.k, out.v, out.weights):
+            x.fill_(7.0)
+    before = [x.cpu() for x in (out.k, out.v)]
+    before_w = out.weights.cpu()
+    idx, new = rtp.cache_evict(cache, torch.tensor(lens, dtype=torch.int32, device=DEV), budget, sink, recent,
+                               out=None if in_place else out)
+    assert new.tolist() == [budget, budget]
+    to = out.table.cpu().long()
+    there_to = (to >= 0) & (to < out.num_pages)
+    for b, n in enumerate(lens):
+        s = torch.arange(n)
+        real = there[b][s // page]
+        for g in range(Hkv):
+            w = torch.where(real, old_w[table[b][s // page].clamp(0, cache.num_pages - 1), g, s % page], -torch.inf)
+            want = SO.evict_slots(w.numpy(), n, budget, sink, recent)
+            assert np.array_equal(idx[b, g].cpu().numpy(), want)
+            for j, slot in enumerate(want):
+                dp, do = to[b, j // out.page_size], j % out.page_size
+                if not there_to[b, j // out.page_size]:
+                    continue
+                sp, so = table[b, slot // page], slot % page
+                moved = bool(real[slot])
+                for x, o, was in zip((out.k, out.v), old, before):
+                    assert torch.equal(x[dp, do, g].cpu(), o[sp, so, g] if moved else was[dp, do, g])
+                assert out.weights[dp, g, do] == (old_w[sp, g, so] if moved else before_w[dp, g, do])
