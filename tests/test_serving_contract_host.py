@@ -2,10 +2,13 @@
 through stand-in tensors (nothing here reaches a device)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 from long_context_hybrid_b200 import serving
+from oracle import serving_oracle as SO
+from serving_bounds import D, o_bound
 
 FAKE = 0x10000                                  # never dereferenced: validation fails first
 
@@ -118,3 +121,33 @@ def test_library_is_there_although_the_module_fails(small_build, tmp_path, monke
         small_build.build()
     assert ctypes.CDLL(small_build.OUT).one() == 1
     assert not small_build.up_to_date()                          # the module is still to be built
+
+
+# ---------------------------------------------------------------------------
+# The bound that the GPU tests use
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", [64, 1500, 9000])
+def test_bound_rejects_what_is_lost(n, dtype):
+    """An output of zeros and one that leaves out 64 keys in the middle are off by
+    more than the bound at many places (where 64 keys weigh 8 u or more); so is one with a gain of 8 steps of the
+    type where values share a sign (8 steps are 16 u |ref|, the bound is a little
+    over 2 u |ref| there; values about 0 leave |ref| below u sum p|v| / 16 u on
+    long rows, and no bound on roundings can tell). The exact one rounded to the
+    type is within it everywhere."""
+    rng = np.random.default_rng(n)
+    q, k, v = (rng.standard_normal(s) for s in ((8, D), (n, D), (n, D)))
+    q *= 1.5
+    for row in q:
+        ref, _, p, pv, size = SO.decode_head(row, k, v, np.arange(n), D ** -0.5)
+        tol = o_bound(ref, pv, size, dtype, np.abs(v).sum(0))
+        rounded = torch.from_numpy(ref).to(dtype).double().numpy()
+        assert (np.abs(rounded - ref) <= tol).all()
+        assert np.mean(np.abs(ref) > tol) > 0.75     # 9000 bf16 keys: a deviation of 0.026, a bound of 0.0035
+        if 64 < n <= 64 / (4 * torch.finfo(dtype).eps):          # 64 keys weigh at least 8 u (bf16: up to 2048 keys)
+            cut = np.r_[0:n // 2, n // 2 + 64:n]
+            less = p[cut] @ v[cut] / p[cut].sum()
+            assert np.mean(np.abs(less - ref) > tol) > 0.1
+        ref, _, p, pv, size = SO.decode_head(row, k, np.abs(v), np.arange(n), D ** -0.5)
+        tol = o_bound(ref, pv, size, dtype, np.abs(v).sum(0))
+        assert np.mean(np.abs(8 * torch.finfo(dtype).eps * ref) > tol) > 0.9
