@@ -222,3 +222,118 @@ def test_eviction_around_missing_pages(in_place):
                 for x, o, was in zip((out.k, out.v), old, before):
                     assert torch.equal(x[dp, do, g].cpu(), o[sp, so, g] if moved else was[dp, do, g])
                 assert out.weights[dp, g, do] == (old_w[sp, g, so] if moved else before_w[dp, g, do])
+
+
+def test_calls_in_the_order_that_the_readme_shows():
+    """The calls one by one, the new token appended before it attends, give what
+    PagedLayer gives: prompts, an eviction, a token."""
+    B, Hq, Hkv, cap, lens = 2, 4, 2, 128, [100, 37]
+    layer, gen = make_layer(B, cap, seed=3, n_obs=16, sink=2)
+    twin, _ = make_layer(B, cap, seed=3)
+    cache, heads = twin.cache, list(range(Hq))
+    q, k, v = (rows(gen, sum(lens), h) for h in (Hq, Hkv, Hkv))
+    q1, k1, v1 = (rows(gen, B, h) for h in (Hq, Hkv, Hkv))
+    cu = torch.tensor([0, 100, 137], dtype=torch.int32, device=DEV)
+    o, o1 = torch.zeros_like(q), torch.zeros_like(q1)
+    layer.prefill(q, k, v, o, cu)
+    kept = layer.evict(50, 10)
+    layer.decode(q1, k1, v1, o1)
+
+    mine, mine1 = torch.zeros_like(q), torch.zeros_like(q1)
+    lse, w = torch.zeros(Hq, sum(lens), device=DEV), torch.zeros(Hkv, sum(lens), device=DEV)
+    pos, cu1 = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 0], [0, 1, 2]))
+    lens_d = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    rtp.attn_packed(q, k, v, mine, heads, cu, lse=lse)
+    rtp.attn_key_weights(q, k, lse, w, heads, cu, n_obs=16)
+    rtp.paged_append(cache, k, v, cu, pos, weights=w)
+    idx, lens_d = rtp.cache_evict(cache, lens_d, 50, sink=2, recent=10)
+    rtp.paged_append(cache, k1, v1, cu1, lens_d)
+    lens_d += 1
+    rtp.paged_attn_decode(q1, cache, lens_d, mine1, heads, weights_out=cache.weights)
+    for a, b in ((o, mine), (kept, idx), (o1, mine1), (layer.lens, lens_d), (layer.cache.k, cache.k),
+                 (layer.cache.v, cache.v), (layer.cache.weights, cache.weights)):
+        assert torch.equal(a, b)
+
+
+def test_captured_eviction_follows_lengths_tables_and_weights():
+    """A captured eviction and the step behind it replay with the lengths, tables,
+    rows and weights that the buffers hold at the replay."""
+    B, Hq, Hkv, cap, budget = 2, 4, 2, 256, 40
+    layer, gen = make_layer(B, cap, Hq, Hkv, sink=3)
+    cache = layer.cache
+    for x in (cache.k, cache.v):
+        x.copy_(torch.randn(x.shape, generator=gen).to(x))
+    q1, k1, v1 = (rows(gen, B, h) for h in (Hq, Hkv, Hkv))
+    o = torch.zeros_like(q1)
+
+    def step():
+        idx = layer.evict(budget, 11)
+        layer.decode(q1, k1, v1, o)
+        return idx
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        idx = step()
+    for lens in ([256, 41], [40, 200], [0, 256], [39, 1]):
+        cache.table.copy_(torch.randperm(cache.num_pages, generator=gen).to(torch.int32).view(B, -1))
+        cache.weights.copy_(torch.rand(cache.weights.shape, generator=gen))
+        layer.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        saved = [x.clone() for x in (cache.k, cache.v, cache.weights, layer.lens)]
+        graph.replay()
+        got = [x.clone() for x in (idx, o, cache.k, cache.v, cache.weights, layer.lens)]
+        for b, n in enumerate(lens):
+            s = torch.arange(n)
+            for g in range(Hkv):
+                w = saved[2].cpu()[cache.table[b].cpu().long()[s // 16], g, s % 16].numpy()
+                want = SO.evict_slots(w, n, budget, 3, 11)
+                assert np.array_equal(got[0][b, g].cpu().numpy()[:len(want)], want)
+        for x, y in zip((cache.k, cache.v, cache.weights, layer.lens), saved):
+            x.copy_(y)
+        o.zero_()
+        again = step()
+        for x, y in zip(got, (again, o, cache.k, cache.v, cache.weights, layer.lens)):
+            assert torch.equal(x, y)
+        assert layer.lens.tolist() == [min(n, budget) + 1 for n in lens]
+
+
+@pytest.mark.parametrize("budget,sink,recent", [(100, 4, 20), (64, 0, 0), (30, 10, 20)])
+def test_a_loops_eviction_keeps_what_its_weights_say(budget, sink, recent):
+    """After prompts and steps, the layer's choice is the oracle's on the weights
+    that the cache holds."""
+    lens, Hq, Hkv = [150, 1, 333], 8, 2
+    layer, gen = make_layer(3, 512, Hq, Hkv, seed=9, sink=sink, n_obs=32)
+    q, k, v = (rows(gen, sum(lens), h, 1.3) for h in (Hq, Hkv, Hkv))
+    cu = torch.tensor([0, 150, 151, 484], dtype=torch.int32, device=DEV)
+    layer.prefill(q, k, v, torch.zeros_like(q), cu)
+    for _ in range(4):
+        q1, k1, v1 = (rows(gen, 3, h, 1.3) for h in (Hq, Hkv, Hkv))
+        layer.decode(q1, k1, v1, torch.zeros_like(q1))
+    w, table = layer.cache.weights.cpu(), layer.cache.table.cpu().long()
+    idx = layer.evict(budget, recent).cpu().numpy()
+    for b, n in enumerate(x + 4 for x in lens):
+        s = torch.arange(n)
+        for g in range(Hkv):
+            want = SO.evict_slots(w[table[b][s // 16], g, s % 16].numpy(), n, budget, sink, recent)
+            assert np.array_equal(idx[b, g][:len(want)], want) and (idx[b, g][len(want):] == -1).all()
+
+
+@pytest.mark.parametrize("cu", [[0, 300, 100, 400], [500, -5, 10 ** 9, 20], [-10, -10, -10, -10], [400, 300, 200, 0],
+                                [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 17], [390, 390, 400, 1000]])
+def test_bad_offsets_of_an_append_stay_inside_the_pages(cu):
+    """Offsets that decrease or leave [0, T] and positions out of range: the pages
+    in front of and behind the pool, and the weights there, are left alone."""
+    T, Hkv, page, n, guard = 400, 2, 16, 80, 8
+    gen = torch.Generator().manual_seed(17)
+    pools = [torch.full((n + 2 * guard, page, Hkv, D), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    weights = torch.full((n + 2 * guard, Hkv, page), 7.0, device=DEV)
+    inner = slice(guard, guard + n)
+    table = torch.randperm(n, generator=gen).to(torch.int32)[:75].view(3, 25).to(DEV)
+    cache = rtp.PagedCache(pools[0][inner], pools[1][inner], table, weights[inner])
+    k, v = rows(gen, T, Hkv), rows(gen, T, Hkv)
+    cu_d = torch.tensor(cu, dtype=torch.int64).to(torch.int32).to(DEV)
+    for pos in ([0, 2 ** 31 - 1, -2 ** 31], [-100, 399, 5], [400, -1, 0]):
+        rtp.paged_append(cache, k, v, cu_d, torch.tensor(pos, dtype=torch.int64).to(torch.int32).to(DEV),
+                         weights=torch.rand(Hkv, T, device=DEV))
+    for x in (*pools, weights):
+        assert (x[:guard] == 7.0).all() and (x[guard + n:] == 7.0).all()
