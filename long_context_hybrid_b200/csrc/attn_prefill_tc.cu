@@ -573,6 +573,11 @@ prefill_attn_tc_kernel(const PrefillAttnParams p, const __grid_constant__ CUtens
 }
 
 namespace {
+// The most shared memory of a block. The sparse kernels' limit is set to it in
+// every call: it is the function's, not the launch's, so another host thread's
+// call with a shorter list would otherwise lower it before this one's launch.
+constexpr size_t kMostSmem = 227 * 1024;
+
 size_t smem_bytes(uint32_t list_off, const PrefillAttnParams& p) {
   return 1024 + list_off + (size_t)p.list_cap * sizeof(int2) + sizeof(Bars);
 }
@@ -583,7 +588,7 @@ size_t smem_bytes(uint32_t list_off, const PrefillAttnParams& p) {
 size_t prefill_attn_tc_smem_bytes(const PrefillAttnParams& p) {
   if (!p.sparse) return smem_bytes(Layout<2, 2>::kListOff, p);
   const size_t s3 = smem_bytes(Layout<1, 3>::kListOff, p);
-  return s3 <= 227 * 1024 ? s3 : smem_bytes(Layout<1, 2>::kListOff, p);
+  return s3 <= kMostSmem ? s3 : smem_bytes(Layout<1, 2>::kListOff, p);
 }
 
 cudaError_t launch_prefill_attn_tc(const PrefillAttnParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
@@ -593,7 +598,7 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnParams& p, const CUtensorMap
   if (p.sparse) {
     const bool three = smem == smem_bytes(Layout<1, 3>::kListOff, p);
     auto kernel = three ? prefill_attn_tc_kernel<1, 3> : prefill_attn_tc_kernel<1, 2>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
     if (e != cudaSuccess) return e;
     dim3 grid((p.Nq + 127) / 128, p.n_heads, B);
     kernel<<<grid, Layout<1, 3>::kThreads, smem, stream>>>(p, tmQ, tmK, tmV, status);

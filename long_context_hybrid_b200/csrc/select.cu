@@ -671,8 +671,12 @@ cudaError_t launch_select_decode(const float* qt, const DecodeQuery* dq, float* 
   // scan: as many CTAs as fit on the GPU at once, each a contiguous run
   const size_t scan_smem = (size_t)max_nj * kBins * sizeof(uint32_t);
   const int64_t total = (int64_t)B * gh.n_ag * L;
+  // the limit of each kernel: the most of any call that takes it, so that
+  // another host thread's smaller call cannot lower it before this launch
+  const int most_nj = max_nj <= 1 ? 1 : max_nj <= 2 ? 2 : max_nj <= 4 ? 4 : kMaxHeadsPerGroup;
+  const int scan_limit = most_nj * kBins * (int)sizeof(uint32_t);
   auto scan = [&](auto kernel) -> cudaError_t {
-    cudaError_t e2 = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scan_smem);
+    cudaError_t e2 = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, scan_limit);
     if (e2 != cudaSuccess) return e2;
     int per_sm = 0;
     e2 = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kScanThreads, scan_smem);

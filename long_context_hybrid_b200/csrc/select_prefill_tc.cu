@@ -366,9 +366,12 @@ cudaError_t launch_select_prefill_tc(const void* qt, const void* kt, int64_t kt_
   if (!make_tmap_index(&tq, qt, B, Hr, N, N, 128) || !make_tmap_index(&tk, kt, B, Hkv, N, kt_cap, kChunkKeys))
     return cudaErrorInvalidValue;
   const size_t smem = select_prefill_tc_smem(p.nb);
-  if (smem > 227 * 1024) return cudaErrorInvalidValue;
+  constexpr size_t kMostSmem = 227 * 1024;
+  if (smem > kMostSmem) return cudaErrorInvalidValue;
+  // the function's limit, not the launch's: the same in every call, so that
+  // another host thread's shorter prompt cannot lower it before this launch
   cudaError_t e = cudaFuncSetAttribute(prefill_select_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       (int)kMostSmem);
   if (e != cudaSuccess) return e;
   e = cudaMemsetAsync(status, 0, sizeof(int), stream);
   if (e != cudaSuccess) return e;

@@ -1,4 +1,5 @@
-"""Calls from other host threads than the one that loaded the library."""
+"""Calls from other host threads than the one that loaded the library, one after
+the other and side by side (the C calls run without the interpreter's lock)."""
 import threading
 
 import pytest
@@ -69,3 +70,94 @@ def test_the_first_cuda_call_of_a_host_thread(name):
     torch.cuda.synchronize()
     assert not raised, raised
     assert torch.equal(out, want)
+
+
+def side_by_side(jobs, repeats):
+    """Each job (C function, its arguments before the stream, its output) in a host
+    thread and on a stream of its own: every call is accepted, and the outputs are
+    those of the job alone."""
+    bad = [[] for _ in jobs]
+    outs = []
+    for call, args, out in jobs:
+        assert call(*args, torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        outs.append(out.clone())
+        out.zero_()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    gate = threading.Barrier(len(jobs))
+
+    def work(i):
+        call, args, _ = jobs[i]
+        gate.wait()
+        for _ in range(repeats):
+            s = call(*args, streams[i].cuda_stream)
+            if s != 0:
+                bad[i].append(s)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not any(bad), f"refused: {[len(b) for b in bad]} of {repeats} each, status {set(sum(bad, []))}"
+    for (_, _, out), want in zip(jobs, outs):
+        assert torch.equal(out, want)
+
+
+def ws_of(n):
+    return torch.zeros(n, dtype=torch.uint8, device=DEV)
+
+
+def test_select_prefill():
+    jobs, keep = [], []
+    for N in (1024, 16384):
+        gen = torch.Generator().manual_seed(N)
+        qt, kt = (torch.randn(1, 1, N, R, generator=gen).to(torch.bfloat16).to(DEV) for _ in range(2))
+        blocks = torch.zeros(1, 1, N // 64, 8, dtype=torch.int32, device=DEV)
+        counts = torch.zeros(1, 1, N // 64, dtype=torch.int32, device=DEV)
+        n = rtp.lib().rtp_workspace_size_select_prefill(1, N, 1, 8)
+        ws = ws_of(n)
+        keep.append((qt, kt, counts, ws))
+        jobs.append((rtp.lib().rtp_select_prefill,
+                     (qt.data_ptr(), kt.data_ptr(), N, 1, N, 1, 1, R, rtp._i32([0]), 8, blocks.data_ptr(),
+                      counts.data_ptr(), ws.data_ptr(), n), blocks))
+    side_by_side(jobs, 3000)
+
+
+def test_sparse_attn_prefill():
+    jobs, keep = [], []
+    for N, topk in ((1024, 1), (16384, 64)):
+        gen = torch.Generator().manual_seed(N)
+        q, k, v = (torch.randn(1, N, 1, D, generator=gen).to(torch.bfloat16).to(DEV) for _ in range(3))
+        o = torch.zeros_like(q)
+        qt, kt = (torch.randn(1, 1, N, R, generator=gen).to(torch.bfloat16).to(DEV) for _ in range(2))
+        blocks, counts = rtp.select_prefill(qt, kt, [0], topk)
+        n = rtp.lib().rtp_workspace_size_sparse_attn_prefill(1, N, 1, topk)
+        ws = ws_of(n)
+        keep.append((q, k, v, o, blocks, counts, ws))
+        s = rtp._strides4
+        jobs.append((rtp.lib().rtp_sparse_attn_prefill,
+                     (q.data_ptr(), s(q), k.data_ptr(), s(k), v.data_ptr(), s(v), o.data_ptr(), s(o), 1, N, 1, 1,
+                      rtp._i32([0]), 1, blocks.data_ptr(), counts.data_ptr(), topk, 2, 1, D ** -0.5, ws.data_ptr(), n),
+                     o))
+    side_by_side(jobs, 2000)
+
+
+@pytest.mark.parametrize("heads", [(3, 4), (5, 16)])
+def test_select_decode(heads):
+    L, topk = 4096, 64
+    jobs, keep = [], []
+    for Hr in heads:
+        gen = torch.Generator().manual_seed(Hr)
+        qt = torch.randn(1, Hr, R, generator=gen).to(DEV)
+        kt = torch.randn(1, 1, L, R, generator=gen).to(torch.bfloat16).to(DEV)
+        idx = torch.zeros(1, Hr, topk, dtype=torch.int32, device=DEV)
+        n = rtp.lib().rtp_workspace_size_select_decode(1, L, Hr, topk)
+        ws = ws_of(n)
+        keep.append((qt, kt, ws))
+        jobs.append((rtp.lib().rtp_select_decode,
+                     (qt.data_ptr(), kt.data_ptr(), L, 1, L, Hr, 1, R, rtp._i32([0] * Hr), topk, idx.data_ptr(),
+                      ws.data_ptr(), n), idx))
+    side_by_side(jobs, 3000)
