@@ -554,7 +554,8 @@ RTP_API rtp_status rtp_swa(const void* q, rtp_strides qs, const void* k, rtp_str
  *   dtype    RTP_BF16 or RTP_F16, one for every 16-bit tensor of a call.
  *            Scores, softmax statistics, sums and weights are fp32; the
  *            softmax's numerators are rounded once to dtype for the product
- *            with v, its denominator takes them unrounded.
+ *            with v, its denominator takes them unrounded. Exponentials are the
+ *            device's approximate 2^x (relative error about 2^-22).
  * Lengths and offsets stay on the device, so a captured graph follows them.
  * They are clamped to the limits passed from the host: bad contents give
  * unspecified rows of the outputs, never an access outside the tensors.

@@ -18,10 +18,11 @@
 // against 610 for 16 prompts of 64 to 8190 tokens, 32 heads, window 1024; 74
 // against 51 for 64 x 128 tokens, 32 heads.)
 //
-// One prompt of 32768 tokens, 32 heads: 7.3 to 7.9 ms, 1.11 to 1.2 PFLOP/s, with
-// the power limit holding the SMs at about 1.6 GHz; smaller calls are bound by
-// the chain of a unit: scores, softmax, product, about 3400 clocks a key tile
-// for both query tiles, of which the exponentials are 2048.
+// One prompt of 32768 tokens, 32 heads: 7.3 to 7.9 ms, 1.11 to 1.2 PFLOP/s, at
+// about 1.6 GHz under the power limit. Bound by the chain of a unit: scores,
+// softmax, product, about 3300 clocks a key tile for both query tiles, of which
+// the exponentials are 2048 and the products 2048; 4230 with a window of 1024,
+// where 40% of the key tiles are cut by a mask and a unit has few of them.
 //
 // Warp roles (384 threads; of 256 with one query tile):
 //   warp 0     producer: finds units, hands them to the other warps through two

@@ -1,7 +1,8 @@
 // The paged cache: filling it and shrinking it.
 //
-// rtp_paged_append copies packed K/V rows (and weights) to their slots; it
-// moves 1 KB per token and KV head and is bound by HBM. A CTA takes up to 32
+// rtp_paged_append copies packed K/V rows (and weights) to their slots, 1 KB
+// moved per token and KV head. Bound by the rounds of a CTA, which wait for one
+// another (26477 tokens of 4 heads: 24.6 us, of HBM's time 16.7). A CTA takes up to 32
 // consecutive tokens: one warp finds their sequences, pages and rows (a lane
 // each), then the warps copy whole rows in 16-byte pieces.
 //
@@ -18,7 +19,8 @@
 //     bits are fewer, but every CTA then reads 64 KB of its neighbours'
 //     histograms a pass: 22 against 16 us for 8 x 4 rows of 5000 to 32768);
 //   * the move, bound by HBM: 512 bytes of K and V read and written per kept
-//     token and KV head (the same rows cut to 8192 each: 43 us, 6.2 TB/s).
+//     token and KV head (the same rows cut to 8192 each, 249 MB both ways: 41 us,
+//     6.1 TB/s). In place it is a chain, a step of 128 rows after another: 221 us.
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
